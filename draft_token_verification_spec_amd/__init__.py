@@ -531,3 +531,9 @@ def sv_workspace_status(workspace: Optional[Workspace], device=None, clear: bool
     _check(_load().sv_workspace_status(_stream(dev), _ptr(ws), ws.numel(), _ptr(out), int(bool(clear))),
            "sv_workspace_status")
     return out
+
+
+from . import attn as _attn  # noqa: E402
+from .attn import *  # noqa: E402,F401,F403
+
+__all__ += _attn.__all__

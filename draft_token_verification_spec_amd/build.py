@@ -2,10 +2,11 @@
 
     python -m draft_token_verification_spec_amd.build
 
-compiles every ``csrc/*.hip`` and ``csrc/api.cpp`` with hipcc into
+compiles every ``csrc/*.hip`` and ``csrc/*.cpp`` with hipcc into
 ``draft_token_verification_spec_amd/libspecverify.so`` (the verification
-library behind ``include/specverify.h``), and ``csrc/bench/*.hip`` into
-``libsvbench.so`` (measurement aids for ``bench.py``: a read-bandwidth probe).
+library behind ``include/specverify.h`` and ``include/specverify_attn.h``),
+and ``csrc/bench/*.hip`` into ``libsvbench.so`` (measurement aids for
+``bench.py``: a read-bandwidth probe).
 Sources are compiled in parallel.
 """
 from __future__ import annotations
@@ -28,7 +29,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function"]
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "api.cpp")]
+    return sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
 def bench_sources():

@@ -1,0 +1,109 @@
+// Tokens of a paged cache read back into contiguous rows.
+//
+// A copy (with a conversion): bound by HBM.  A workgroup takes kRows output
+// rows; each row's sequence and page are found once, by one wave per two
+// rows, and then all threads move 8 channels at a time, a thread keeping its
+// head and channels over the rows so that its loads do not wait for one
+// another.
+#include "sv_attn.hpp"
+
+namespace sv {
+
+namespace {
+
+constexpr int kGatherThreads = 256;
+constexpr int kRows = 8;
+
+// 8 stored channels at offset `off` of a cache as the output's type.
+template <bool FP8, typename OT>
+__device__ __forceinline__ void copy8(const void* base, int64_t off, uint32_t biased, OT* out) {
+  uint4 w;
+  if (FP8)
+    w = dequant8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + off), scale_of(biased));
+  else
+    w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
+  if (sizeof(OT) == 2) {
+    *reinterpret_cast<uint4*>(out) = w;
+  } else {
+    const float y[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
+                        bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+    store8(reinterpret_cast<float*>(out), y);
+  }
+}
+
+template <typename OT>
+__device__ __forceinline__ void zero8(OT* out) {
+  uint4* p = reinterpret_cast<uint4*>(out);
+  p[0] = make_uint4(0u, 0u, 0u, 0u);
+  if (sizeof(OT) == 4) p[1] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <bool FP8, typename OT>
+__global__ __launch_bounds__(kGatherThreads) void gather_kernel(GatherArgs a, int lg_cols) {
+  __shared__ int where[kRows][2];  // page (-1: zeros, -2: not a row of ours), slot
+  const PagedView& c = a.cache;
+  const int t0 = blockIdx.x * kRows;
+  const int lane = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < kRows; r += kGatherThreads / 64) {
+    const int t = t0 + r;
+    int page = -2, place = 0;
+    if (t < a.T) {
+      const int b = find_sequence(a.row_start, a.B, t, lane);
+      if (b >= 0 && t < a.row_start[b + 1]) {
+        place = int(uint32_t(a.kv_begin ? a.kv_begin[b] : 0) + uint32_t(t - a.row_start[b]));
+        page = page_of(c, b, place);
+      }
+    }
+    if (lane == 0) {
+      where[r][0] = page;
+      where[r][1] = place & ((1 << c.page_shift) - 1);
+    }
+  }
+  __syncthreads();
+  const int chunks = c.heads * (c.D >> 3);  // of 8 channels in a row
+  const int cols = 1 << lg_cols;
+  for (int i = threadIdx.x & (cols - 1); i < chunks; i += cols) {
+    const int h = i / (c.D >> 3), e0 = (i - h * (c.D >> 3)) * 8;
+#pragma unroll 4
+    for (int r = threadIdx.x >> lg_cols; r < kRows; r += kGatherThreads >> lg_cols) {
+      const int page = where[r][0], slot = where[r][1];
+      if (page == -2) continue;
+      const int64_t at = int64_t(t0 + r) * (c.heads * c.D) + i * 8;
+      OT* ko = static_cast<OT*>(a.k_out) + at;
+      OT* vo = static_cast<OT*>(a.v_out) + at;
+      if (page < 0) {
+        if (a.k_out) zero8(ko);
+        if (a.v_out) zero8(vo);
+        continue;
+      }
+      const int64_t scale_at = ((int64_t(page) * c.heads + h) << c.page_shift) + slot;
+      if (a.k_out)
+        copy8<FP8>(c.k, page * c.k_page + slot * c.k_token + h * c.k_head + e0, FP8 ? c.k_scale[scale_at] : 0u, ko);
+      if (a.v_out)
+        copy8<FP8>(c.v, page * c.v_page + slot * c.v_token + h * c.v_head + e0, FP8 ? c.v_scale[scale_at] : 0u, vo);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_gather(const GatherArgs& a, int out_dtype, int cache_dtype, hipStream_t stream) {
+  const int chunks = a.cache.heads * (a.cache.D >> 3);
+  int lg = 0;
+  while ((1 << lg) < chunks && (1 << lg) < kGatherThreads) ++lg;
+  const dim3 grid((a.T - 1) / kRows + 1), block(kGatherThreads);
+  if (cache_dtype == SV_E4M3) {
+    if (out_dtype == SV_BF16)
+      hipLaunchKernelGGL((gather_kernel<true, uint16_t>), grid, block, 0, stream, a, lg);
+    else
+      hipLaunchKernelGGL((gather_kernel<true, float>), grid, block, 0, stream, a, lg);
+  } else {
+    if (out_dtype == SV_BF16)
+      hipLaunchKernelGGL((gather_kernel<false, uint16_t>), grid, block, 0, stream, a, lg);
+    else
+      hipLaunchKernelGGL((gather_kernel<false, float>), grid, block, 0, stream, a, lg);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace sv

@@ -1,0 +1,67 @@
+// Launchers of the rotary, cache and attention kernels (attn_api.cpp checks
+// the arguments).
+#pragma once
+
+#include "sv_paged.hpp"
+
+namespace sv {
+
+// Rows x [T, heads, D] with strides between rows and heads, in elements.
+struct RowsIn {
+  const void* p;
+  int64_t token, head;
+};
+struct RowsOut {
+  void* p;
+  int64_t token, head;
+};
+
+struct RopeArgs {
+  int T, heads, D, rotary;
+  int layout, backward;
+  RowsIn x;
+  RowsOut out;
+  const int64_t* positions;
+  const double* freq;
+  float mscale;
+};
+hipError_t launch_rope(const RopeArgs& a, int dtype, hipStream_t stream);
+
+struct AppendArgs {
+  int B, T, q_heads, rotary;
+  int layout;
+  const double* freq;
+  float mscale;
+  const int64_t* positions;  // nullable
+  RowsIn q, k, v;
+  RowsOut q_out;
+  const int32_t* query_start;
+  const int32_t* kv_len;
+  PagedView cache;
+};
+hipError_t launch_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
+
+struct GatherArgs {
+  int B, T;
+  const int32_t* row_start;
+  const int32_t* kv_begin;  // nullable
+  void* k_out;              // nullable
+  void* v_out;              // nullable
+  PagedView cache;
+};
+hipError_t launch_gather(const GatherArgs& a, int out_dtype, int cache_dtype, hipStream_t stream);
+
+struct AttnArgs {
+  int B, T, q_heads;
+  RowsIn q;
+  RowsOut out;
+  float* lse;  // nullable
+  const int32_t* query_start;
+  const int32_t* kv_len;
+  float scale;
+  int window;  // 0: none
+  PagedView cache;
+};
+hipError_t launch_attention(const AttnArgs& a, int cache_dtype, hipStream_t stream);
+
+}  // namespace sv
