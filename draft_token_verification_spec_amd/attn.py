@@ -39,7 +39,7 @@ SV_E4M3 = 2
 SV_ATTN_MAX_HEAD_DIM = 256
 SV_ATTN_MAX_HEADS = 1024
 SV_ATTN_MAX_PAGE = 65536
-SV_ATTN_MAX_TOKENS = 2147483647
+SV_ATTN_MAX_TOKENS = 1073741824
 SV_ATTN_MAX_ROWS = 1 << 23
 SV_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 SV_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
@@ -343,6 +343,8 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if want_lse:
         _need(o, "lse", (T, q_heads), torch.float32, dev)
     lp = _array(dev, "out['lse']", o["lse"], torch.float32, T, q_heads) if "lse" in o else None
+    if max_kv_len == 0:
+        max_kv_len = cache.max_pages * cache.page_size
     nbytes = _attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, cache.heads, D, max_q_len, max_kv_len)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace.get(dev, nbytes)
     _call(dev, "sv_paged_attention", B, T, q_heads, *qp, ctypes.addressof(cache), qs, kl, max_q_len, max_kv_len,

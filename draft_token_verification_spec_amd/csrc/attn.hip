@@ -1,8 +1,29 @@
 // Causal attention of packed new tokens over a paged cache.
 //
-// One workgroup per row and query head: a thread scores one token of a block
-// of 256 at a time, the softmax runs online (running maximum and sum), and the
-// weighted values are summed with a thread per channel.
+// For a request b and key / value head kvh, the n new tokens and the
+// G = q_heads / heads query heads of the group make R = n * G rows that read
+// the same keys and values: row r is token r / G, head kvh * G + r % G.  A
+// workgroup takes a tile of kRowTile rows and a range of tokens (a split).
+//
+// Scores are formed transposed, S^T = K Q^T, so that a lane of the matrix
+// instruction's result holds one row (lane & 15) and four tokens: the softmax
+// statistics of a row are one value per lane, its running maximum a reduction
+// inside the lane and over the four lanes of the row, and the weights are
+// already the B operand of O^T += V^T P^T (the order of the tokens inside a
+// product's inner dimension is free as long as both operands agree).  Only
+// V^T needs its elements transposed, which the transposing LDS reads do.
+//
+// Few rows (up to 64 a request and head): HBM-bound.  The four waves take
+// blocks of 32 tokens in turn, each with its own running statistics, so that
+// no wave waits for another until their results are joined at the end; keys go
+// from memory to registers directly in the A operand's layout (a lane's 16
+// bytes of one token's row), values through the wave's own part of LDS.  A
+// wave asks for the next block's keys and values as soon as the present ones
+// have left their registers.
+//
+// Splits: where rows are few and contexts long, a context is divided into
+// ranges of `split_len` tokens, whose results (running maximum, sum, weighted
+// values in binary32) a second kernel joins.
 #include "sv_attn.hpp"
 
 namespace sv {
@@ -10,100 +31,490 @@ namespace sv {
 namespace {
 
 constexpr int kAttnThreads = 256;
+constexpr int kAttnWaves = kAttnThreads / 64;
+constexpr int kBlock = 32;  // tokens a wave takes at a time
 
-template <bool FP8>
-__device__ __forceinline__ void cache8(const void* base, int64_t off, uint32_t biased, float (&x)[8]) {
-  uint4 w;
-  if (FP8)
-    w = dequant8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + off), scale_of(biased));
-  else
-    w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
-  x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-  x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// One tile of rows of one request, as every kernel sees it.
+struct Tile {
+  int b, first_row;      // request, tile's first row in it (row = token * G + head in group)
+  int rows;              // rows of the tile, <= kRowTile; 0: nothing to do
+  int token0;            // the request's first packed row
+  int place0;            // place of the request's first new token
+  int begin, end;        // tokens that some row of the tile may see
+  int held;              // tokens of the request in the cache
+};
+
+// Slot `slot` of the launch: the tiles of request b take the slots from
+// query_start[b] * G / kRowTile + b on, which leaves room for all of them
+// (ceil(n G / M) <= floor((s + n) G / M) - floor(s G / M) + 1) and grows
+// strictly with b.  By the whole wave.
+template <int M>
+__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int G, int slot, int lane) {
+  Tile t;
+  t.rows = 0;
+  int lo = 0, hi = a.B;
+  auto first_slot = [&](int b) { return int64_t(a.query_start[b]) * G / M + b; };
+  while (lo < hi) {
+    const int step = (hi - lo + 63) >> 6;
+    const int at = lo + lane * step;
+    const bool in = at < hi;
+    const int n = __popcll(__ballot(in && first_slot(in ? at : lo) <= slot));
+    if (n == 0) break;
+    const int base = lo;
+    lo = base + (n - 1) * step + 1;
+    hi = min(hi, base + n * step);
+  }
+  t.b = lo - 1;
+  if (t.b < 0) return t;
+  t.token0 = a.query_start[t.b];
+  const int64_t n = int64_t(a.query_start[t.b + 1]) - t.token0;
+  const int64_t first = (slot - first_slot(t.b)) * M;
+  const int64_t rows = n * G - first;
+  if (t.token0 < 0 || int64_t(t.token0) + n > a.T || rows <= 0) return t;
+  t.first_row = int(first);
+  t.rows = int(min(rows, int64_t(M)));
+  const int64_t len = max(a.kv_len[t.b], 0);
+  t.held = int(max(int64_t(0), min(len, int64_t(a.cache.max_pages) << a.cache.page_shift)));
+  const int64_t place0 = len - n;
+  t.place0 = int(place0);
+  const int64_t first_place = place0 + first / G, last_place = place0 + (first + t.rows - 1) / G;
+  t.end = int(max(int64_t(0), min(int64_t(t.held), last_place + 1)));
+  t.begin = a.window > 0 ? int(min(int64_t(t.end), max(int64_t(0), first_place - a.window + 1))) : 0;
+  return t;
 }
 
-template <bool FP8>
-__global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnArgs a) {
-  __shared__ float q[SV_ATTN_MAX_HEAD_DIM];
-  __shared__ float p[kAttnThreads];
-  __shared__ int pages[kAttnThreads];
-  __shared__ float red[kAttnThreads / 64];
+// The splits that have tokens of [begin, end): first .. last (empty: 0 .. 0).
+struct Splits {
+  int first, last;
+};
+__device__ __forceinline__ Splits live_splits(const Tile& t, int split_len, int num_splits) {
+  if (t.begin >= t.end) return {0, 0};
+  return {min(t.begin / split_len, num_splits - 1), min((t.end - 1) / split_len, num_splits - 1)};
+}
+
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {  // either packed bf16 is infinite or NaN
+  return ((w & 0x7f80u) == 0x7f80u) | ((w & 0x7f800000u) == 0x7f800000u);
+}
+__device__ __forceinline__ bool not_finite8(const uint4& w) {
+  return (not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w)) != 0;
+}
+
+__device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+
+// 4 x 16 elements of LDS transposed: each group of 16 lanes reads 4 rows of 16
+// bf16 (lane i the 4 from column 4 (i % 4) of row i / 4) and gets column i.
+__device__ __forceinline__ uint2 read_transposed(const uint16_t* p) {
+  const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4*)(const_cast<uint16_t*>(p)));
+  return __builtin_bit_cast(uint2, r);
+}
+
+// Where element e of a value row lies in LDS: rows of DP elements, their
+// 32-byte units permuted by the row so that the rows that one transposing read
+// takes (and one store writes) fall on different banks.
+template <int DP>
+__device__ __forceinline__ int value_at(int row, int e) {
+  const int flip = DP == 64 ? (row >> 1) & 3 : row & 7;
+  return row * DP + (e ^ (flip << 4));
+}
+
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+
+template <int DP, int MT, bool FP8>
+__global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) void few_rows_kernel(AttnArgs a, AttnPlan p) {
+  constexpr int M = 16 * MT;
+  constexpr int kSteps = DP / 32;        // of the score product
+  constexpr int kDT = DP / 16;           // channel tiles of the result
+  constexpr int kLoads = FP8 ? DP / 64 : DP / 32;  // 16-byte loads of a token's row per lane
+  __shared__ __align__(16) uint16_t values[kAttnWaves][kBlock * DP];
+  __shared__ float stat_m[kAttnWaves][M], stat_l[kAttnWaves][M];
+
   const PagedView& c = a.cache;
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
-  const int b = find_sequence(a.query_start, a.B, t, lane);
-  if (b < 0 || t >= a.query_start[b + 1]) return;
-  const int64_t cap = int64_t(c.max_pages) << c.page_shift;
-  const int held = int(max(int64_t(0), min(int64_t(a.kv_len[b]), cap)));
-  const int place = int(uint32_t(a.kv_len[b]) - uint32_t(a.query_start[b + 1] - t));
-  const int end = int(min(int64_t(place) + 1, int64_t(held)));
-  const int begin = a.window > 0 ? max(0, int(max(int64_t(0), int64_t(place) + 1 - a.window))) : 0;
-  const int kvh = h / (a.q_heads / c.heads);
-  if (tid < c.D) q[tid] = load1(static_cast<const uint16_t*>(a.q.p) + t * a.q.token + h * a.q.head + tid) * (a.scale * kLog2e);
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j0 = begin; j0 < end; j0 += kAttnThreads) {
-    __syncthreads();
-    const int j = j0 + tid;
-    const int page = j < end ? page_of(c, b, j) : -1;
-    const int slot = j & ((1 << c.page_shift) - 1);
-    float s = -INFINITY;
-    if (page >= 0) {
-      s = 0.f;
-      const int64_t off = page * c.k_page + slot * c.k_token + kvh * c.k_head;
-      const uint32_t biased = FP8 ? c.k_scale[((int64_t(page) * c.heads + kvh) << c.page_shift) + slot] : 0u;
-      for (int e = 0; e < c.D; e += 8) {
-        float k8[8];
-        cache8<FP8>(c.k, off + e, biased, k8);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int G = a.q_heads / c.heads;
+  const Tile t = find_tile<M>(a, G, blockIdx.x, lane);
+  if (t.rows == 0) return;
+  const Splits live = live_splits(t, p.split_len, p.num_splits);
+  if (split < live.first || split > live.last) return;
+  const int begin = max(t.begin, split * p.split_len) & ~(kBlock - 1);
+  const int end = split == p.num_splits - 1 ? t.end : min(int64_t(t.end), int64_t(split + 1) * p.split_len);
+
+  // queries: the B operand, lane (row, g) holding the channels of its steps
+  const int chunks = c.D >> 3;
+  uint4 qf[MT][kSteps];
+  int place[MT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += q[e + i] * k8[i];
-      }
-    }
-    pages[tid] = page;
-    float top = s == s ? s : INFINITY;  // a NaN score must not be passed over by the maximum
-    for (int i = 32; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
-    if (lane == 0) red[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    if (top == -INFINITY) continue;
-    const float m2 = fmaxf(m, top);
-    const float w = s == -INFINITY ? 0.f : fast_exp2(s - m2);
-    p[tid] = w;
-    const float keep = m == -INFINITY ? 0.f : fast_exp2(m - m2);
-    m = m2;
-    __syncthreads();
-    if (lane == 0) red[tid >> 6] = 0.f;
-    float sum = wave_sum(w);
-    if (lane == 0) red[tid >> 6] = sum;
-    __syncthreads();
-    l = l * keep + red[0] + red[1] + red[2] + red[3];
-    o *= keep;
-    if (tid < c.D) {
-      for (int i = 0; i < kAttnThreads && j0 + i < end; ++i) {
-        if (pages[i] < 0) continue;
-        const int sl = (j0 + i) & ((1 << c.page_shift) - 1);
-        const int64_t off = pages[i] * c.v_page + sl * c.v_token + kvh * c.v_head;
-        const uint32_t biased = FP8 ? c.v_scale[((int64_t(pages[i]) * c.heads + kvh) << c.page_shift) + sl] : 0u;
-        float v8[8];
-        cache8<FP8>(c.v, off + (tid & ~7), biased, v8);
-        float v = v8[0];
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + r;
+    const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
+    place[m] = row < t.rows ? t.place0 + tok : -1;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
 #pragma unroll
-        for (int k = 1; k < 8; ++k) v = (tid & 7) == k ? v8[k] : v;
-        o += p[i] * v;
-      }
+    for (int s = 0; s < kSteps; ++s) {
+      const int ch = FP8 ? 8 * (s >> 1) + 2 * g + (s & 1) : 4 * s + g;
+      qf[m][s] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < t.rows && ch < chunks) qf[m][s] = *reinterpret_cast<const uint4*>(q + 8 * ch);
     }
   }
-  if (tid < c.D) store1(static_cast<uint16_t*>(a.out.p) + t * a.out.token + h * a.out.head + tid, l == 0.f ? 0.f : o / l);
-  if (a.lse && tid == 0)
-    a.lse[int64_t(t) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
+  const int first_place = t.place0 + t.first_row / G;  // the places of the tile's first and last rows
+  const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
+  const float sc = a.scale * kLog2e;
+
+  f32x4 o[kDT][MT];
+  float mx[MT], l[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    mx[m] = -INFINITY;
+    l[m] = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  uint4 kr[2][kLoads], vr[2][kLoads];
+  uint32_t ks[2] = {127, 127}, vs[2] = {127, 127};
+  bool have[2];
+  // the pages of the block's tokens r and 16 + r (-1: absent)
+  auto pages = [&](int base, int (&page)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) page[h] = base < end ? page_of(c, t.b, base + 16 * h + r) : -1;
+  };
+  // ask for a block's rows; the loads of absent tokens and of channels beyond
+  // the head's go to page 0 and to its last channels, and are not used
+  auto request = [&](int base, const int (&page)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = max(page[h], 0), slot = (base + 16 * h + r) & ((1 << c.page_shift) - 1);
+      have[h] = page[h] >= 0 && base + 16 * h + r < end;
+      const int64_t ko = at * c.k_page + slot * c.k_token + kvh * c.k_head;
+      const int64_t vo = at * c.v_page + slot * c.v_token + kvh * c.v_head;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int unit = min(4 * i + g, (FP8 ? c.D >> 4 : c.D >> 3) - 1);  // of 16 bytes
+        kr[h][i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.k) + (FP8 ? ko : 2 * ko) + 16 * unit);
+        vr[h][i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.v) + (FP8 ? vo : 2 * vo) + 16 * unit);
+      }
+      if (FP8) {
+        const int64_t so = ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot;
+        ks[h] = c.k_scale[so];
+        vs[h] = c.v_scale[so];
+      }
+    }
+  };
+
+  const int stride = kAttnWaves * kBlock;
+  int base = begin + wave * kBlock;
+  int page[2];
+  pages(base, page);
+  if (base < end) request(base, page);
+  pages(base + stride, page);
+  uint16_t* const mine = values[wave];
+  for (; base < end; base += stride) {
+    // S^T, a block's 16 tokens by 16 rows at a time
+    f32x4 s[2][MT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) s[h][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const float kscale = FP8 ? scale_of(ks[h]) : 1.f;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        uint4 kf;
+        if (FP8) {
+          const uint4 w = kr[h][st >> 1];
+          kf = dequant8((st & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), kscale);
+        } else {
+          kf = kr[h][st];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s[h][m] = mfma16(kf, qf[m][st], s[h][m]);
+      }
+    }
+    // every row sees every token of the block, unless it reaches beyond the
+    // first row's place or the last row's window, or lacks tokens
+    const bool whole = __all(have[0] && have[1]) && base + kBlock - 1 <= first_place &&
+                       (a.window == 0 || base > last_place - a.window);
+    uint32_t hidden = 0, nan = 0;  // bit 16 h + i: token 16 h + i is absent; its value is not finite
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 w[kLoads * (FP8 ? 2 : 1)];
+      if (FP8) {
+        const float vscale = scale_of(vs[h]);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          w[2 * i] = dequant8(make_uint2(vr[h][i].x, vr[h][i].y), vscale);
+          w[2 * i + 1] = dequant8(make_uint2(vr[h][i].z, vr[h][i].w), vscale);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) w[i] = vr[h][i];
+      }
+      if (!whole) {
+        // a weight of zero does not stop a value that is not finite: such
+        // values are taken out, and their tokens' scores made NaN instead
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kLoads * (FP8 ? 2 : 1); ++i) bad |= not_finite8(w[i]);
+        uint64_t any = __ballot(bad && have[h]);
+        any |= any >> 32;
+        any |= any >> 16;
+        nan |= uint32_t(any & 0xffffu) << (16 * h);
+        hidden |= uint32_t(~__ballot(have[h]) & 0xffffu) << (16 * h);
+        const bool drop = !have[h] || ((any >> r) & 1u);
+#pragma unroll
+        for (int i = 0; i < kLoads * (FP8 ? 2 : 1); ++i)
+          if (drop) w[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads * (FP8 ? 2 : 1); ++i) {
+        const int ch = FP8 ? 8 * (i >> 1) + 2 * g + (i & 1) : 4 * i + g;
+        *reinterpret_cast<uint4*>(mine + value_at<DP>(16 * h + r, 8 * ch)) = w[i];
+      }
+    }
+    const int now = base;
+    if (base + stride < end) {
+      request(base + stride, page);
+      pages(base + 2 * stride, page);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = 16 * h + 4 * g + i, j = now + k;
+          const bool off = (hidden >> k) & 1u, bad = (nan >> k) & 1u;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const bool sees = !off && j <= place[m] && (a.window == 0 || j > place[m] - a.window);
+            s[h][m][i] = sees ? (bad ? NAN : s[h][m][i]) : -INFINITY;
+          }
+        }
+    }
+    // weights, in place of the scores, and the running statistics
+    uint4 pf[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[h][m][i]);
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float next = fmaxf(mx[m], top);
+      const float ref = next == -INFINITY ? 0.f : next * sc;
+      const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
+      mx[m] = next;
+      float sum = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[h][m][i] = fast_exp2(fmaf(s[h][m][i], sc, -ref));
+          sum += s[h][m][i];
+        }
+      l[m] = fmaf(l[m], keep, sum);
+      // rounded to bf16 for the product: a weight of at most 1 is off by 2^-8 of itself
+      pf[m] = make_uint4(pack_bf16(s[0][m][0], s[0][m][1]), pack_bf16(s[0][m][2], s[0][m][3]),
+                         pack_bf16(s[1][m][0], s[1][m][1]), pack_bf16(s[1][m][2], s[1][m][3]));
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
+    }
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) {
+      const int e = 16 * d + 4 * (r & 3);
+      const uint2 v0 = read_transposed(mine + value_at<DP>(4 * g + (r >> 2), e));
+      const uint2 v1 = read_transposed(mine + value_at<DP>(16 + 4 * g + (r >> 2), e));
+      const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) o[d][m] = mfma16(vf, pf[m], o[d][m]);
+    }
+  }
+
+  // join the waves: the tile's maximum, then each wave's results scaled to it
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    l[m] += __shfl_xor(l[m], 16, 64);
+    l[m] += __shfl_xor(l[m], 32, 64);
+    if (g == 0) {
+      stat_m[wave][16 * m + r] = mx[m];
+      stat_l[wave][16 * m + r] = l[m];
+    }
+  }
+  __syncthreads();
+  const bool alone = live.first == live.last;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + r;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][row]);
+    const float ref = top == -INFINITY ? 0.f : top * sc;
+    const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
+    float* part = reinterpret_cast<float*>(values[wave]);  // [16][DP] as channels by rows
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[(16 * d + 4 * g + i) * 16 + r] = o[d][m][i] * keep;
+    __syncthreads();
+    // 16 rows by 16 threads, 8 channels at a time
+    const int orow = threadIdx.x & 15;
+    const int trow = 16 * m + orow;
+    if (trow < t.rows) {
+      float rtop = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) rtop = fmaxf(rtop, stat_m[w][trow]);
+      const float rref = rtop == -INFINITY ? 0.f : rtop * sc;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) total += stat_l[w][trow] * fast_exp2(fmaf(stat_m[w][trow], sc, -rref));
+      const int tok = t.token0 + (t.first_row + trow) / G, head = kvh * G + (t.first_row + trow) % G;
+      const int64_t at = int64_t(tok) * a.q_heads + head;
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      for (int ch = threadIdx.x >> 4; ch < chunks; ch += 16) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          y[j] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kAttnWaves; ++w)
+            y[j] += reinterpret_cast<const float*>(values[w])[(8 * ch + j) * 16 + orow];
+          if (alone) y[j] *= inv;
+        }
+        if (alone)
+          store8(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + 8 * ch, y);
+        else
+          store8(p.part_o + (split * (int64_t(a.T) * a.q_heads) + at) * c.D + 8 * ch, y);
+      }
+      if (threadIdx.x < 16) {
+        if (!alone)
+          p.part_ml[split * (int64_t(a.T) * a.q_heads) + at] = make_float2(rtop == -INFINITY ? rtop : rref, total);
+        else if (a.lse)
+          a.lse[at] = total == 0.f ? -INFINITY : (rref + fast_log2(total)) * kLn2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// joining splits
+// ---------------------------------------------------------------------------
+
+// One wave per row and head: the splits' maxima and sums give each split's
+// weight, then the weighted values are summed, four channels a lane.
+template <int M>
+__global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan p) {
+  const PagedView& c = a.cache;
+  const int lane = threadIdx.x & 63;
+  const int64_t at = int64_t(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
+  const int64_t all = int64_t(a.T) * a.q_heads;
+  if (at >= all) return;
+  const int tok = int(at / a.q_heads), head = int(at % a.q_heads);
+  const int G = a.q_heads / c.heads;
+  const int b = find_sequence(a.query_start, a.B, tok, lane);
+  if (b < 0 || tok >= a.query_start[b + 1]) return;
+  // the row's tile, as the kernel that wrote the parts saw it
+  const int64_t row = int64_t(tok - a.query_start[b]) * G + head % G;
+  const Tile t = find_tile<M>(a, G, int(int64_t(a.query_start[b]) * G / M + b + row / M), lane);
+  if (t.rows == 0) return;
+  const Splits live = live_splits(t, p.split_len, p.num_splits);
+  if (live.first == live.last) return;  // written by the split itself
+  float top = -INFINITY;
+  for (int s = live.first; s <= live.last; ++s) top = fmaxf(top, p.part_ml[s * all + at].x);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float total = 0.f, y[4] = {};
+  const bool mine = 4 * lane < c.D;
+  for (int s = live.first; s <= live.last; ++s) {
+    const float2 ml = p.part_ml[s * all + at];
+    const float w = fast_exp2(ml.x - ref);
+    total = fmaf(w, ml.y, total);
+    if (mine) {
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + 4 * lane);
+      y[0] = fmaf(w, v.x, y[0]), y[1] = fmaf(w, v.y, y[1]), y[2] = fmaf(w, v.z, y[2]), y[3] = fmaf(w, v.w, y[3]);
+    }
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  if (mine)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head +
+                              4 * lane) =
+        make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+  if (a.lse && lane == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
+}
+
+template <int DP, int MT, bool FP8>
+void launch_few(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  const int G = a.q_heads / a.cache.heads;
+  const dim3 grid(int64_t(a.T) * G / (16 * MT) + a.B, a.cache.heads, p.num_splits), block(kAttnThreads);
+  hipLaunchKernelGGL((few_rows_kernel<DP, MT, FP8>), grid, block, 0, stream, a, p);
+  if (p.num_splits > 1) {
+    const dim3 jgrid((int64_t(a.T) * a.q_heads + kAttnWaves - 1) / kAttnWaves);
+    hipLaunchKernelGGL(join_kernel<16 * MT>, jgrid, block, 0, stream, a, p);
+  }
+}
+
+template <int DP, bool FP8>
+void launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  if (p.row_tiles == 1)
+    launch_few<DP, 1, FP8>(a, p, stream);
+  else if (p.row_tiles == 2)
+    launch_few<DP, 2, FP8>(a, p, stream);
+  else if constexpr (DP < 256)
+    launch_few<DP, 4, FP8>(a, p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_attention(const AttnArgs& a, int cache_dtype, hipStream_t stream) {
-  const dim3 grid(a.T, a.q_heads), block(kAttnThreads);
-  if (cache_dtype == SV_E4M3)
-    hipLaunchKernelGGL(attention_kernel<true>, grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL(attention_kernel<false>, grid, block, 0, stream, a);
+AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len) {
+  AttnPlan p;
+  const int G = q_heads / kv_heads;
+  if (max_q_len <= 0 || max_q_len > T) max_q_len = B > 0 ? (T + B - 1) / B : T;
+  const int64_t rows = int64_t(max_q_len) * G;
+  p.row_tiles = rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4;
+  // enough workgroups for every compute unit several times over, of at least
+  // 256 tokens each
+  const int64_t tiles = (int64_t(T) * G / (16 * p.row_tiles) + (B < T ? B : T)) * kv_heads;
+  const int64_t most = (int64_t(max_kv_len) + 255) / 256;
+  int64_t n = tiles > 0 ? (2048 + tiles - 1) / tiles : 1;
+  n = n < most ? n : most;
+  n = n < 1 ? 1 : n;
+  int64_t len = (max_kv_len + n - 1) / n;
+  len = (len + 127) / 128 * 128;
+  p.split_len = int(len < 128 ? 128 : len > (1 << 30) ? (1 << 30) : len);
+  p.num_splits = int((int64_t(max_kv_len) + p.split_len - 1) / p.split_len);
+  if (p.num_splits < 1) p.num_splits = 1;
+  const size_t rows_all = size_t(T) * q_heads;
+  p.ml_bytes = p.num_splits > 1 ? (size_t(p.num_splits) * rows_all * sizeof(float2) + 255) / 256 * 256 : 0;
+  p.o_bytes = p.num_splits > 1 ? (size_t(p.num_splits) * rows_all * D * sizeof(float) + 255) / 256 * 256 : 0;
+  p.part_ml = nullptr;
+  p.part_o = nullptr;
+  return p;
+}
+
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream) {
+  if (cache_dtype == SV_E4M3) {
+    if (a.cache.D <= 64)
+      launch_rows<64, true>(a, p, stream);
+    else if (a.cache.D <= 128)
+      launch_rows<128, true>(a, p, stream);
+    else
+      launch_rows<256, true>(a, p, stream);
+  } else {
+    if (a.cache.D <= 64)
+      launch_rows<64, false>(a, p, stream);
+    else if (a.cache.D <= 128)
+      launch_rows<128, false>(a, p, stream);
+    else
+      launch_rows<256, false>(a, p, stream);
+  }
   return hipGetLastError();
 }
 

@@ -55,7 +55,7 @@ PagedView view_of(const sv_paged_cache* c) {
   PagedView v;
   v.table = c->page_table;
   v.table_stride = c->page_table_stride;
-  v.max_pages = c->max_pages;
+  v.max_pages = c->num_pages > 0 ? c->max_pages : 0;  // a cache without pages holds nothing
   v.num_pages = c->num_pages;
   v.heads = c->heads;
   v.D = c->head_dim;
@@ -220,7 +220,8 @@ int sv_kv_gather(void* stream, int B, int T, int out_dtype, const sv_paged_cache
 size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim, int max_q_len,
                                          int max_kv_len) {
   if (check_attention_sizes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len) != SV_OK) return 0;
-  return 256;
+  const AttnPlan p = plan_attention(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
+  return 256 + p.ml_bytes + p.o_bytes;
 }
 
 int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
@@ -241,10 +242,10 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
   for (int64_t s : {q_token_stride, q_head_stride, out_token_stride, out_head_stride})
     if (s < 0 || s % 8 != 0) return SV_ERR_INVALID_ARG;
   if (!write_strides_ok(T, q_heads, cache->head_dim, out_token_stride, out_head_stride)) return SV_ERR_INVALID_ARG;
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < sv_paged_attention_workspace_size(B, T, q_heads, cache->heads, cache->head_dim, max_q_len,
-                                                          max_kv_len))
-    return SV_ERR_WORKSPACE;
+  AttnPlan p = plan_attention(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < 256 + p.ml_bytes + p.o_bytes) return SV_ERR_WORKSPACE;
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
   AttnArgs a;
   a.B = B;
   a.T = T;
@@ -257,7 +258,7 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
   a.scale = scale;
   a.window = window;
   a.cache = view_of(cache);
-  return to_status(launch_attention(a, cache->dtype, static_cast<hipStream_t>(stream)));
+  return to_status(launch_attention(a, p, cache->dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

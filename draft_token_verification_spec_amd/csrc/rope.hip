@@ -170,8 +170,7 @@ __global__ __launch_bounds__(kRopeThreads) void append_kernel(AppendArgs a) {
   if (b < 0) return;
   const int end = a.query_start[b + 1];
   if (t >= end) return;  // behind the last sequence
-  // both ends of this difference are caller data: unsigned, so that it wraps
-  const int place = int(uint32_t(a.kv_len[b]) - uint32_t(end - t));
+  const int place = max(a.kv_len[b], 0) - (end - t);
   const int page = page_of(a.cache, b, place);
   const double position = a.positions ? double(a.positions[t]) : double(place);
   make_angles(cs, a.freq, a.rotary >> 1, position, a.mscale, 1.f);

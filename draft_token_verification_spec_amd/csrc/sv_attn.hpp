@@ -62,6 +62,17 @@ struct AttnArgs {
   int window;  // 0: none
   PagedView cache;
 };
-hipError_t launch_attention(const AttnArgs& a, int cache_dtype, hipStream_t stream);
+
+// How a call is divided: 16 * row_tiles rows a workgroup, contexts in splits
+// of split_len tokens (the last one takes what is left).  The parts of split s
+// and row t, head h are at (s * T + t) * q_heads + h.
+struct AttnPlan {
+  int row_tiles, split_len, num_splits;
+  size_t ml_bytes, o_bytes;
+  float2* part_ml;  // maximum (base-2 logarithm), sum of weights
+  float* part_o;    // weighted values
+};
+AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len);
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream);
 
 }  // namespace sv

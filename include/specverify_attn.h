@@ -30,7 +30,8 @@
  *
  * Places.  kv_len[b] (int32 [B]) is the number of tokens of request b in the
  * cache, its new ones included: row i of its n rows is at place
- * kv_len[b] - n + i.  Rows at negative places are not stored and see nothing.
+ * kv_len[b] - n + i (a negative kv_len counts as 0).  Rows at negative places
+ * are not stored and see nothing.
  */
 #ifndef SPECVERIFY_ATTN_H
 #define SPECVERIFY_ATTN_H
@@ -51,7 +52,7 @@ extern "C" {
 #define SV_ATTN_MAX_HEAD_DIM 256
 #define SV_ATTN_MAX_HEADS 1024
 #define SV_ATTN_MAX_PAGE 65536
-#define SV_ATTN_MAX_TOKENS 2147483647
+#define SV_ATTN_MAX_TOKENS 1073741824
 #define SV_ATTN_MAX_ROWS (1 << 23)
 
 /* A paged cache of keys and values, with the page table of the requests of a
@@ -179,8 +180,9 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * (q . k_j)),
  *   lse = log(sum_j w_j)   (natural logarithm).
  * A row that sees no token gets out = 0 and lse = -infinity.  A token that a
- * row does not see has no influence on it, whatever its key and value hold; a
- * row that sees a key or value that is not finite gets no finite result.
+ * row does not see has no influence on it, whatever its key and value hold.  A
+ * NaN that a row sees shows: one in a key makes its whole result NaN, one in a
+ * value the channel's at least.
  *   q, out     SV_BF16 elements, [T, q_heads, head_dim] with the given
  *              strides, 16-byte aligned, strides multiples of 8 elements;
  *              q_heads a multiple of cache->heads.
