@@ -406,6 +406,280 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
 }
 
 // ---------------------------------------------------------------------------
+// many rows
+// ---------------------------------------------------------------------------
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+
+// Where element e of a key row lies in LDS: 16-byte units permuted by the row
+// so that 16 rows' units of the same channels fall on different banks.
+template <int DP>
+__device__ __forceinline__ int key_at(int row, int e) {
+  const int flip = DP == 64 ? (row >> 1) & 7 : row & 15;
+  return row * DP + (e ^ (flip << 3));
+}
+
+constexpr int kTile = 64;      // tokens of a tile
+constexpr int kManyRows = 32 * kAttnWaves;
+
+template <int DP, bool FP8>
+__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kernel(AttnArgs a, AttnPlan p) {
+  constexpr int M = kManyRows;
+  constexpr int kSteps = DP / 16;
+  constexpr int kDT = DP / 32;
+  constexpr int kLanes = FP8 ? DP / 16 : DP / 8;      // that load a token's row, 16 bytes each
+  constexpr int kSpan = kAttnThreads / kLanes;        // tokens of one load of the workgroup
+  constexpr int kLoads = kTile / kSpan;
+  constexpr int kParts = FP8 ? 2 : 1;                 // 8 channels each, of a load
+  __shared__ __align__(16) uint16_t keys[2][kTile * DP];
+  __shared__ __align__(16) uint16_t values[2][kTile * DP];
+  __shared__ __align__(16) uint8_t state[2][kTile];   // of a token: 0 present, 1 absent, 2 a value not finite
+  __shared__ __align__(16) int lacks[2][kAttnWaves];  // some token that this wave loaded is absent
+
+  const PagedView& c = a.cache;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 31, h = lane >> 5;
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int G = a.q_heads / c.heads;
+  // later tiles of a prompt see more: they start first
+  const Tile t = find_tile<M>(a, G, gridDim.x - 1 - blockIdx.x, lane);
+  if (t.rows == 0) return;
+  const Splits live = live_splits(t, p.split_len, p.num_splits);
+  if (split < live.first || split > live.last) return;
+  const int begin = max(t.begin, split * p.split_len) & ~(kTile - 1);
+  const int end = split == p.num_splits - 1 ? t.end : min(int64_t(t.end), int64_t(split + 1) * p.split_len);
+
+  const int chunks = c.D >> 3;
+  const int row = 32 * wave + r;
+  const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
+  const int place = row < t.rows ? t.place0 + tok : -1;
+  uint4 qf[kSteps];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      qf[s] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < t.rows && 2 * s + h < chunks) qf[s] = *reinterpret_cast<const uint4*>(q + 8 * (2 * s + h));
+    }
+  }
+  const int first_place = t.place0 + t.first_row / G;
+  const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
+  // of this wave's rows
+  const int wave_first = t.place0 + (t.first_row + 32 * wave) / G;
+  const int wave_last = 32 * wave < t.rows ? t.place0 + (t.first_row + min(32 * wave + 31, t.rows - 1)) / G : -1;
+  const float sc = a.scale * kLog2e;
+
+  f32x16 o[kDT];
+#pragma unroll
+  for (int d = 0; d < kDT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float mx = -INFINITY, l = 0.f;
+
+  // staging: thread -> token kSpan * i + tid / kLanes, 16 bytes tid % kLanes
+  const int unit = min(tid % kLanes, (FP8 ? c.D >> 4 : chunks) - 1);
+  uint4 kr[kLoads], vr[kLoads];
+  uint32_t ks[kLoads], vs[kLoads];
+  int page[kLoads];
+  auto pages = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = base + kSpan * i + tid / kLanes;
+      page[i] = j < end ? page_of(c, t.b, j) : -1;
+    }
+  };
+  uint32_t absent;  // bit i: load i's token is absent
+  auto request = [&](int base) {
+    absent = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = base + kSpan * i + tid / kLanes;
+      absent |= uint32_t(page[i] < 0) << i;
+      const int at = max(page[i], 0), slot = j & ((1 << c.page_shift) - 1);
+      const int64_t ko = at * c.k_page + slot * c.k_token + kvh * c.k_head;
+      const int64_t vo = at * c.v_page + slot * c.v_token + kvh * c.v_head;
+      kr[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.k) + (FP8 ? ko : 2 * ko) + 16 * unit);
+      vr[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.v) + (FP8 ? vo : 2 * vo) + 16 * unit);
+      if (FP8) {
+        const int64_t so = ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot;
+        ks[i] = c.k_scale[so];
+        vs[i] = c.v_scale[so];
+      }
+    }
+  };
+  // every row of the tile sees all 64 tokens, as far as places go
+  auto whole = [&](int base) {
+    return base + kTile - 1 <= first_place && base + kTile <= end && (a.window == 0 || base > last_place - a.window);
+  };
+  auto stage = [&](int base, int buf) {
+    const bool ok = whole(base);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = kSpan * i + tid / kLanes;
+      uint4 kw[kParts], vw[kParts];
+      if (FP8) {
+        kw[0] = dequant8(make_uint2(kr[i].x, kr[i].y), scale_of(ks[i]));
+        kw[kParts - 1] = dequant8(make_uint2(kr[i].z, kr[i].w), scale_of(ks[i]));
+        vw[0] = dequant8(make_uint2(vr[i].x, vr[i].y), scale_of(vs[i]));
+        vw[kParts - 1] = dequant8(make_uint2(vr[i].z, vr[i].w), scale_of(vs[i]));
+      } else {
+        kw[0] = kr[i];
+        vw[0] = vr[i];
+      }
+      const bool gone = (absent >> i) & 1u;
+      bool bad = false;
+      if (!ok) {
+        // a weight of zero does not stop a value that is not finite: such
+        // values are taken out, and their tokens' scores made NaN instead
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) bad |= not_finite8(vw[q]);
+        const uint64_t any = __ballot(bad && !gone);
+        bad = (any >> (lane & ~(kLanes - 1))) & ((uint64_t(1) << kLanes) - 1);
+      }
+      if (gone || bad) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) vw[q] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) {
+        const int e = 8 * (kParts * (tid % kLanes) + q);
+        *reinterpret_cast<uint4*>(&keys[buf][key_at<DP>(at, e)]) = kw[q];
+        *reinterpret_cast<uint4*>(&values[buf][value_at<DP>(at, e)]) = vw[q];
+      }
+      if (tid % kLanes == 0) state[buf][at] = gone ? 1 : bad ? 2 : 0;
+    }
+    const bool some = __any(absent != 0);
+    if (lane == 0) lacks[buf][wave] = some;
+  };
+
+  int buf = 0;
+  pages(begin);
+  if (begin < end) {
+    request(begin);
+    pages(begin + kTile);
+    stage(begin, 0);
+  }
+  __syncthreads();
+  for (int base = begin; base < end; base += kTile) {
+    const bool more = base + kTile < end;
+    if (more) {
+      request(base + kTile);
+      pages(base + 2 * kTile);
+    }
+    // a wave whose rows see nothing here only helps to load
+    if (base <= wave_last && (a.window == 0 || base + kTile - 1 > wave_first - a.window)) {
+      const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
+      const bool masked = !whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0;
+      f32x16 s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4 kf = *reinterpret_cast<const uint4*>(&keys[buf][key_at<DP>(32 * u + r, 8 * (2 * st + h))]);
+          s[u] = mfma32(kf, qf[st], s[u]);
+        }
+      if (masked) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(&state[buf][32 * u + 8 * k + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = base + 32 * u + 8 * k + 4 * h + i;
+              const uint32_t is = (w >> (8 * i)) & 0xffu;
+              const bool sees = is != 1 && j <= place && (a.window == 0 || j > place - a.window);
+              s[u][4 * k + i] = sees ? (is == 2 ? NAN : s[u][4 * k + i]) : -INFINITY;
+            }
+          }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      if (__any(top > mx)) {
+        const float next = fmaxf(mx, top);
+        const float keep = fast_exp2((mx - (next == -INFINITY ? 0.f : next)) * sc);
+        mx = next;
+        l *= keep;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) o[d] *= keep;
+      }
+      const float ref = mx == -INFINITY ? 0.f : mx * sc;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[u][i] = fast_exp2(fmaf(s[u][i], sc, -ref));
+          l += s[u][i];
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          // rounded to bf16 for the product: a weight of at most 1 is off by 2^-8 of itself
+          const uint4 pf = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
+                                      pack_bf16(s[u][8 * q + 4], s[u][8 * q + 5]),
+                                      pack_bf16(s[u][8 * q + 6], s[u][8 * q + 7]));
+          const int at = 32 * u + 16 * q + 4 * h + ((lane & 15) >> 2);
+#pragma unroll
+          for (int d = 0; d < kDT; ++d) {
+            const int e = 32 * d + (lane & 16) + 4 * (lane & 3);
+            const uint2 v0 = read_transposed(&values[buf][value_at<DP>(at, e)]);
+            const uint2 v1 = read_transposed(&values[buf][value_at<DP>(at + 8, e)]);
+            o[d] = mfma32(make_uint4(v0.x, v0.y, v1.x, v1.y), pf, o[d]);
+          }
+        }
+    }
+    if (more) stage(base + kTile, buf ^ 1);
+    buf ^= 1;
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (row >= t.rows) return;
+  const float ref = mx == -INFINITY ? 0.f : mx * sc;
+  const int64_t at = int64_t(t.token0 + tok) * a.q_heads + head;
+  if (live.first == live.last) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* out = static_cast<uint16_t*>(a.out.p) + int64_t(t.token0 + tok) * a.out.token + head * a.out.head;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = 32 * d + 8 * k + 4 * h;
+        if (e < c.D)
+          *reinterpret_cast<uint2*>(out + e) = make_uint2(pack_bf16(o[d][4 * k] * inv, o[d][4 * k + 1] * inv),
+                                                          pack_bf16(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv));
+      }
+    if (a.lse && h == 0) a.lse[at] = l == 0.f ? -INFINITY : (ref + fast_log2(l)) * kLn2;
+  } else {
+    const int64_t part = split * (int64_t(a.T) * a.q_heads) + at;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = 32 * d + 8 * k + 4 * h;
+        if (e < c.D)
+          *reinterpret_cast<float4*>(p.part_o + part * c.D + e) =
+              make_float4(o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]);
+      }
+    if (h == 0) p.part_ml[part] = make_float2(mx == -INFINITY ? mx : ref, l);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // joining splits
 // ---------------------------------------------------------------------------
 
@@ -450,25 +724,33 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan
   if (a.lse && lane == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
 }
 
+template <int M>
+void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  if (p.num_splits == 1) return;
+  const dim3 grid((int64_t(a.T) * a.q_heads + kAttnWaves - 1) / kAttnWaves), block(kAttnThreads);
+  hipLaunchKernelGGL(join_kernel<M>, grid, block, 0, stream, a, p);
+}
+
 template <int DP, int MT, bool FP8>
-void launch_few(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  const int G = a.q_heads / a.cache.heads;
-  const dim3 grid(int64_t(a.T) * G / (16 * MT) + a.B, a.cache.heads, p.num_splits), block(kAttnThreads);
-  hipLaunchKernelGGL((few_rows_kernel<DP, MT, FP8>), grid, block, 0, stream, a, p);
-  if (p.num_splits > 1) {
-    const dim3 jgrid((int64_t(a.T) * a.q_heads + kAttnWaves - 1) / kAttnWaves);
-    hipLaunchKernelGGL(join_kernel<16 * MT>, jgrid, block, 0, stream, a, p);
-  }
+void launch_few(const AttnArgs& a, const AttnPlan& p, const dim3& grid, hipStream_t stream) {
+  hipLaunchKernelGGL((few_rows_kernel<DP, MT, FP8>), grid, dim3(kAttnThreads), 0, stream, a, p);
+  launch_join<16 * MT>(a, p, stream);
 }
 
 template <int DP, bool FP8>
 void launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  if (p.row_tiles == 1)
-    launch_few<DP, 1, FP8>(a, p, stream);
-  else if (p.row_tiles == 2)
-    launch_few<DP, 2, FP8>(a, p, stream);
-  else if constexpr (DP < 256)
-    launch_few<DP, 4, FP8>(a, p, stream);
+  const int64_t G = a.q_heads / a.cache.heads;
+  const dim3 grid(a.T * G / p.row_tile + a.B, a.cache.heads, p.num_splits);
+  if (p.row_tile == 16) {
+    launch_few<DP, 1, FP8>(a, p, grid, stream);
+  } else if (p.row_tile == 32) {
+    launch_few<DP, 2, FP8>(a, p, grid, stream);
+  } else if (p.row_tile == kManyRows) {
+    hipLaunchKernelGGL((many_rows_kernel<DP, FP8>), grid, dim3(kAttnThreads), 0, stream, a, p);
+    launch_join<kManyRows>(a, p, stream);
+  } else if constexpr (DP < 256) {
+    launch_few<DP, 4, FP8>(a, p, grid, stream);
+  }
 }
 
 }  // namespace
@@ -478,12 +760,13 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   const int G = q_heads / kv_heads;
   if (max_q_len <= 0 || max_q_len > T) max_q_len = B > 0 ? (T + B - 1) / B : T;
   const int64_t rows = int64_t(max_q_len) * G;
-  p.row_tiles = rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4;
+  p.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && D <= 128 ? 64 : kManyRows;
   // enough workgroups for every compute unit several times over, of at least
   // 256 tokens each
-  const int64_t tiles = (int64_t(T) * G / (16 * p.row_tiles) + (B < T ? B : T)) * kv_heads;
+  const int64_t tiles = (int64_t(T) * G / p.row_tile + (B < T ? B : T)) * kv_heads;
   const int64_t most = (int64_t(max_kv_len) + 255) / 256;
-  int64_t n = tiles > 0 ? (2048 + tiles - 1) / tiles : 1;
+  const int64_t want = p.row_tile == kManyRows ? 512 : 2048;
+  int64_t n = tiles > 0 ? (want + tiles - 1) / tiles : 1;
   n = n < most ? n : most;
   n = n < 1 ? 1 : n;
   int64_t len = (max_kv_len + n - 1) / n;

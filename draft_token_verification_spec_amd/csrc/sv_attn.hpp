@@ -63,11 +63,11 @@ struct AttnArgs {
   PagedView cache;
 };
 
-// How a call is divided: 16 * row_tiles rows a workgroup, contexts in splits
+// How a call is divided: row_tile rows a workgroup, contexts in splits
 // of split_len tokens (the last one takes what is left).  The parts of split s
 // and row t, head h are at (s * T + t) * q_heads + h.
 struct AttnPlan {
-  int row_tiles, split_len, num_splits;
+  int row_tile, split_len, num_splits;
   size_t ml_bytes, o_bytes;
   float2* part_ml;  // maximum (base-2 logarithm), sum of weights
   float* part_o;    // weighted values
