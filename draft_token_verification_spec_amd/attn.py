@@ -12,6 +12,7 @@ passed as its ``transpose(1, 2)``): bfloat16, or float8_e4m3fn with ``k_scale``,
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -52,14 +53,6 @@ _f = ctypes.c_float
 _d = ctypes.c_double
 
 
-class _PagedCache(ctypes.Structure):  # sv_paged_cache
-    _fields_ = [("dtype", _i), ("heads", _i), ("head_dim", _i), ("page_size", _i), ("num_pages", _i),
-                ("max_pages", _i), ("page_table", _p), ("page_table_stride", _i64), ("k", _p), ("v", _p),
-                ("k_page_stride", _i64), ("k_token_stride", _i64), ("k_head_stride", _i64),
-                ("v_page_stride", _i64), ("v_token_stride", _i64), ("v_head_stride", _i64),
-                ("k_scale", _p), ("v_scale", _p)]
-
-
 _SIGNATURES = {
     "sv_rope_frequencies": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, _p]),
     "sv_rope": (_i, [_p, _i, _i, _i, _i, _i, _i, _i, _p, _i64, _i64, _p, _p, _f, _p, _i64, _i64]),
@@ -89,50 +82,62 @@ def _attn_lib():
 # ---------------------------------------------------------------------------
 # marshalling helpers
 # ---------------------------------------------------------------------------
+#
+# A call's own time on the host is that of a few microseconds' kernel, so the
+# checks read each attribute once and devices are compared by their index.
 
-def _on(dev: torch.device, name: str, t: torch.Tensor, *dtypes):
-    """``t`` is on the call's device, of one of ``dtypes``."""
+def _tensor(name: str, t) -> int:
+    """The index of the HIP device that holds ``t``."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev or dev.type != "cuda":
-        raise ValueError(f"{name} must live on the call's HIP device (got {t.device}, the call is on {dev})")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))} (got {t.dtype})")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must live on a HIP device (got {t.device})")
+    return dev
 
 
-def _array(dev: torch.device, name: str, t: torch.Tensor, dtype: torch.dtype, *shape) -> int:
+def _refuse(dev: int, name: str, t, dtype):
+    """Why ``t`` is not a tensor of ``dtype`` on device ``dev``."""
+    if _tensor(name, t) != dev:
+        raise ValueError(f"{name} must live on the call's HIP device cuda:{dev} (got {t.device})")
+    raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+
+
+def _array(dev: int, name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
     """A contiguous array of exactly ``shape``; its address."""
-    _on(dev, name, t, dtype)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype:
+        _refuse(dev, name, t, dtype)
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} (got {list(t.shape)})")
     return t.data_ptr()
 
 
-def _rows(dev: torch.device, name: str, t: torch.Tensor, dtype: torch.dtype, T: int, heads: int, D: int):
+def _rows(dev: int, name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple):
     """Rows [T, heads, D] with contiguous channels; (address, row stride, head stride)."""
-    _on(dev, name, t, dtype)
-    if t.shape != (T, heads, D):
-        raise ValueError(f"{name} must be {[T, heads, D]} (got {list(t.shape)})")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype:
+        _refuse(dev, name, t, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     token, head, one = t.stride()
-    if one != 1 and D > 1:
+    if one != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have unit stride along the channels")
     return t.data_ptr(), token, head
 
 
-def _dtype_code(name: str, t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _three(name: str, t: torch.Tensor) -> tuple:
+    """(T, heads, D) of rows."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim] (got {list(shape)})")
+    return shape
+
+
+def _dtype_code(name: str, dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return SV_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return SV_F32
-    raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
-
-
-def _three(name: str, t: torch.Tensor):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows, heads, head_dim] (got {list(t.shape)})")
-    return t.shape
+    raise TypeError(f"{name} must be bfloat16 or float32 (got {dtype})")
 
 
 def _layout(layout: str) -> int:
@@ -142,64 +147,84 @@ def _layout(layout: str) -> int:
         raise ValueError(f"layout must be one of {sorted(SV_ROPE_LAYOUTS)} (got {layout!r})") from None
 
 
-def _freq(dev: torch.device, freq: Optional[torch.Tensor]):
+def _freq(dev: int, freq: Optional[torch.Tensor]):
     """(address, turned channels) of a frequency table."""
     if freq is None:
         return None, 0
-    _on(dev, "freq", freq, torch.float64)
+    if not isinstance(freq, torch.Tensor) or freq.get_device() != dev or freq.dtype != torch.float64:
+        _refuse(dev, "freq", freq, torch.float64)
     if freq.dim() != 1 or not freq.is_contiguous():
         raise ValueError("freq must be a contiguous 1-D table")
     return freq.data_ptr(), 2 * freq.shape[0]
 
 
-def _paged(dev: torch.device, B: int, k_cache, v_cache, page_table, k_scale, v_scale) -> _PagedCache:
-    _on(dev, "k_cache", k_cache, torch.bfloat16, torch.float8_e4m3fn)
-    _on(dev, "v_cache", v_cache, k_cache.dtype)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+# sv_paged_cache, as bytes: heads and head_dim are fields 1 and 2, max_pages and page_size 5 and 3
+_CACHE = struct.Struct("@6iPqPP6qPP")
+
+
+def _paged(dev: int, B: int, k_cache, v_cache, page_table, k_scale, v_scale):
+    """(sv_paged_cache, heads, head_dim, page table's tokens)."""
+    _tensor("k_cache", k_cache)
+    kind = k_cache.dtype
+    if kind != torch.bfloat16 and kind != torch.float8_e4m3fn or k_cache.get_device() != dev:
+        _refuse(dev, "k_cache", k_cache, "bfloat16 or float8_e4m3fn")
+    if not isinstance(v_cache, torch.Tensor) or v_cache.get_device() != dev or v_cache.dtype != kind:
+        _refuse(dev, "v_cache", v_cache, kind)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, heads, head_dim], both alike")
-    pages, page_size, heads, D = k_cache.shape
+    pages, page_size, heads, D = shape
     kp, kt, kh, k1 = k_cache.stride()
     vp, vt, vh, v1 = v_cache.stride()
     if k1 != 1 or v1 != 1:
         raise ValueError("k_cache and v_cache must have unit stride along the channels")
-    _on(dev, "page_table", page_table, torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must be [{B}, max_pages] (got {list(page_table.shape)})")
-    max_pages = page_table.shape[1]
-    if page_table.stride(1) != 1 and max_pages > 1:
+    if not isinstance(page_table, torch.Tensor) or page_table.get_device() != dev or page_table.dtype != torch.int32:
+        _refuse(dev, "page_table", page_table, torch.int32)
+    tshape = page_table.shape
+    if len(tshape) != 2 or tshape[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages] (got {list(tshape)})")
+    max_pages = tshape[1]
+    table_stride, one = page_table.stride()
+    if one != 1 and max_pages > 1:
         raise ValueError("page_table must have unit stride along the pages")
-    table_stride = page_table.stride(0) if B > 1 else max_pages
-    fp8 = k_cache.dtype == torch.float8_e4m3fn
-    if fp8:
+    # strides along dimensions of one element say nothing: torch may give any
+    if B <= 1:
+        table_stride = max_pages
+    if page_size == 1:
+        kt = vt = D
+    if heads == 1:
+        kh = vh = D
+    if pages <= 1:
+        kp = vp = page_size * heads * D
+    if kind == torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
             raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
-        ks = _array(dev, "k_scale", k_scale, torch.uint8, pages, heads, page_size)
-        vs = _array(dev, "v_scale", v_scale, torch.uint8, pages, heads, page_size)
+        code = SV_E4M3
+        ks = _array(dev, "k_scale", k_scale, torch.uint8, (pages, heads, page_size))
+        vs = _array(dev, "v_scale", v_scale, torch.uint8, (pages, heads, page_size))
     else:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        ks = vs = None
-    # strides along dimensions of one element say nothing: torch may give any
-    if page_size == 1:
-        kt, vt = D, D
-    if heads == 1:
-        kh, vh = D, D
-    if pages <= 1:
-        kp, vp = page_size * heads * D, page_size * heads * D
-    return _PagedCache(SV_E4M3 if fp8 else SV_BF16, heads, D, page_size, pages, max_pages, page_table.data_ptr(),
-                       table_stride, k_cache.data_ptr(), v_cache.data_ptr(), kp, kt, kh, vp, vt, vh, ks, vs)
+        code, ks, vs = SV_BF16, 0, 0
+    return _CACHE.pack(code, heads, D, page_size, pages, max_pages, page_table.data_ptr(), table_stride,
+                       k_cache.data_ptr(), v_cache.data_ptr(), kp, kt, kh, vp, vt, vh, ks, vs), heads, D, \
+        max_pages * page_size
 
 
-def _call(dev: torch.device, what: str, *args):
+def _stream_of(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _call(dev: int, what: str, *args):
     """Call the C entry point on the device's current stream, with the device current."""
-    fn = getattr(_attn_lib(), what)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        status = fn(stream, *args)
+    fn = getattr(_lib or _attn_lib(), what)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(_stream_of(dev), *args)
     else:
         with torch.cuda.device(dev):
-            status = fn(stream, *args)
-    _check(status, what)
+            status = fn(_stream_of(dev), *args)
+    if status != 0:
+        _check(status, what)
 
 
 # ---------------------------------------------------------------------------
@@ -229,17 +254,17 @@ def sv_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, lay
     channels / 2] on the device (``sv_rope_frequencies``).  ``backward``: ``x``
     is the gradient with respect to the output, and the gradient with respect
     to the input is returned.  ``out`` may be ``x``."""
-    T, heads, D = _three("x", x)
-    dev = x.device
-    dtype = _dtype_code("x", x)
-    xp, xt, xh = _rows(dev, "x", x, x.dtype, T, heads, D)
-    pos = _array(dev, "positions", positions, torch.int64, T)
+    dev = _tensor("x", x)
+    shape = T, heads, D = _three("x", x)
+    dtype = x.dtype
+    code = _dtype_code("x", dtype)
+    xr = _rows(dev, "x", x, dtype, shape)
+    pos = _array(dev, "positions", positions, torch.int64, (T,))
     fp, rotary = _freq(dev, freq)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=x.dtype, device=dev)
-    op, ot, oh = _rows(dev, "out", out, x.dtype, T, heads, D)
-    _call(dev, "sv_rope", T, heads, D, rotary, _layout(layout), int(bool(backward)), dtype, xp, xt, xh, pos, fp,
-          mscale, op, ot, oh)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    _call(dev, "sv_rope", T, heads, D, rotary, _layout(layout), 1 if backward else 0, code, *xr, pos, fp, mscale,
+          *_rows(dev, "out", out, dtype, shape))
     return out
 
 
@@ -254,28 +279,31 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     positions if ``freq`` is given; see ``sv_kv_append``.  ``q`` [T, q_heads,
     head_dim]: queries to turn likewise, returned as ``q`` (rows of no request
     are not written).  ``positions`` int64 [T], default: the tokens' places."""
-    T, heads, D = _three("k", k)
-    dev = k.device
+    dev = _tensor("k", k)
+    shape = T, heads, D = _three("k", k)
+    _tensor("kv_len", kv_len)
     B = kv_len.numel()
-    cache = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
-    if (cache.heads, cache.head_dim) != (heads, D):
-        raise ValueError(f"k is {list(k.shape)}, the cache has {cache.heads} heads of {cache.head_dim} channels")
-    dtype = _dtype_code("k", k)
-    kr = _rows(dev, "k", k, k.dtype, T, heads, D)
-    vr = _rows(dev, "v", v, k.dtype, T, heads, D)
+    cache, cache_heads, cache_dim, _ = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
+    if heads != cache_heads or D != cache_dim:
+        raise ValueError(f"k is {list(shape)}, the cache has {cache_heads} heads of {cache_dim} channels")
+    dtype = k.dtype
+    code = _dtype_code("k", dtype)
+    kr = _rows(dev, "k", k, dtype, shape)
+    vr = _rows(dev, "v", v, dtype, shape)
     fp, rotary = _freq(dev, freq)
-    pos = None if positions is None else _array(dev, "positions", positions, torch.int64, T)
-    qs = _array(dev, "query_start", query_start, torch.int32, B + 1)
-    kl = _array(dev, "kv_len", kv_len, torch.int32, B)
+    pos = None if positions is None else _array(dev, "positions", positions, torch.int64, (T,))
+    qs = _array(dev, "query_start", query_start, torch.int32, (B + 1,))
+    kl = _array(dev, "kv_len", kv_len, torch.int32, (B,))
     o = {} if out is None else out
     q_heads, qr, qo = 0, (None, 0, 0), (None, 0, 0)
     if q is not None:
+        _tensor("q", q)
         q_heads = _three("q", q)[1]
-        qr = _rows(dev, "q", q, k.dtype, T, q_heads, D)
-        _need(o, "q", (T, q_heads, D), q.dtype, dev)
-        qo = _rows(dev, "out['q']", o["q"], k.dtype, T, q_heads, D)
-    _call(dev, "sv_kv_append", B, T, q_heads, dtype, rotary, _layout(layout), fp, mscale, pos, *qr, *qo, *kr, *vr, qs,
-          kl, ctypes.addressof(cache))
+        qr = _rows(dev, "q", q, dtype, (T, q_heads, D))
+        _need(o, "q", (T, q_heads, D), dtype, q.device)
+        qo = _rows(dev, "out['q']", o["q"], dtype, (T, q_heads, D))
+    _call(dev, "sv_kv_append", B, T, q_heads, code, rotary, _layout(layout), fp, mscale, pos, *qr, *qo, *kr, *vr, qs,
+          kl, cache)
     return o
 
 
@@ -287,23 +315,22 @@ def sv_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     head_dim] of ``dtype`` (bfloat16 or float32); see ``sv_kv_gather``.
     ``row_start`` int32 [B + 1]; ``kv_begin`` int32 [B], default 0.  Rows
     outside ``row_start`` are not written."""
-    dev = k_cache.device
-    if not isinstance(row_start, torch.Tensor) or row_start.numel() < 1:
-        raise ValueError("row_start must be an int32 tensor of B + 1 entries")
+    dev = _tensor("k_cache", k_cache)
+    _tensor("row_start", row_start)
     B = row_start.numel() - 1
-    cache = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
-    rs = _array(dev, "row_start", row_start, torch.int32, B + 1)
-    kb = None if kv_begin is None else _array(dev, "kv_begin", kv_begin, torch.int32, B)
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"dtype must be bfloat16 or float32 (got {dtype})")
+    if B < 0:
+        raise ValueError("row_start must have B + 1 entries")
+    cache, heads, D, _ = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
+    rs = _array(dev, "row_start", row_start, torch.int32, (B + 1,))
+    kb = None if kv_begin is None else _array(dev, "kv_begin", kv_begin, torch.int32, (B,))
+    code = _dtype_code("dtype", dtype)
     o = {} if out is None else out
-    shape = (rows, cache.heads, cache.head_dim)
-    _need(o, "k", shape, dtype, dev)
-    _need(o, "v", shape, dtype, dev)
-    ko = _array(dev, "out['k']", o["k"], dtype, *shape)
-    vo = _array(dev, "out['v']", o["v"], dtype, *shape)
-    _call(dev, "sv_kv_gather", B, rows, SV_BF16 if dtype == torch.bfloat16 else SV_F32, ctypes.addressof(cache), rs,
-          kb, ko, vo)
+    shape = (rows, heads, D)
+    device = k_cache.device
+    _need(o, "k", shape, dtype, device)
+    _need(o, "v", shape, dtype, device)
+    _call(dev, "sv_kv_gather", B, rows, code, cache, rs, kb, _array(dev, "out['k']", o["k"], dtype, shape),
+          _array(dev, "out['v']", o["v"], dtype, shape))
     return o
 
 
@@ -328,25 +355,30 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     Without a ``workspace`` the call takes one from torch's allocator for its
     own duration: calls on different streams, and captured graphs, then share
     nothing.  A Workspace serves one stream's calls, as everywhere."""
-    T, q_heads, D = _three("q", q)
-    dev = q.device
+    dev = _tensor("q", q)
+    shape = T, q_heads, D = _three("q", q)
+    _tensor("kv_len", kv_len)
     B = kv_len.numel()
-    cache = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
-    if cache.head_dim != D:
-        raise ValueError(f"q is {list(q.shape)}, the cache has heads of {cache.head_dim} channels")
-    qp = _rows(dev, "q", q, torch.bfloat16, T, q_heads, D)
-    qs = _array(dev, "query_start", query_start, torch.int32, B + 1)
-    kl = _array(dev, "kv_len", kv_len, torch.int32, B)
+    cache, heads, cache_dim, tokens = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
+    if cache_dim != D:
+        raise ValueError(f"q is {list(shape)}, the cache has heads of {cache_dim} channels")
+    qr = _rows(dev, "q", q, torch.bfloat16, shape)
+    qs = _array(dev, "query_start", query_start, torch.int32, (B + 1,))
+    kl = _array(dev, "kv_len", kv_len, torch.int32, (B,))
     o = {} if out is None else out
-    _need(o, "out", (T, q_heads, D), torch.bfloat16, dev)
-    op = _rows(dev, "out['out']", o["out"], torch.bfloat16, T, q_heads, D)
+    device = q.device
+    _need(o, "out", shape, torch.bfloat16, device)
+    orows = _rows(dev, "out['out']", o["out"], torch.bfloat16, shape)
     if want_lse:
-        _need(o, "lse", (T, q_heads), torch.float32, dev)
-    lp = _array(dev, "out['lse']", o["lse"], torch.float32, T, q_heads) if "lse" in o else None
+        _need(o, "lse", (T, q_heads), torch.float32, device)
+    lse = _array(dev, "out['lse']", o["lse"], torch.float32, (T, q_heads)) if "lse" in o else None
     if max_kv_len == 0:
-        max_kv_len = cache.max_pages * cache.page_size
-    nbytes = _attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, cache.heads, D, max_q_len, max_kv_len)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if workspace is None else workspace.get(dev, nbytes)
-    _call(dev, "sv_paged_attention", B, T, q_heads, *qp, ctypes.addressof(cache), qs, kl, max_q_len, max_kv_len,
-          D ** -0.5 if scale is None else scale, window, *op, lp, ws.data_ptr(), ws.numel())
+        max_kv_len = tokens
+    nbytes = _attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, heads, D, max_q_len, max_kv_len)
+    if workspace is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        ws = workspace.get(device, nbytes)
+    _call(dev, "sv_paged_attention", B, T, q_heads, *qr, cache, qs, kl, max_q_len, max_kv_len,
+          D ** -0.5 if scale is None else scale, window, *orows, lse, ws.data_ptr(), ws.numel())
     return o

@@ -21,6 +21,14 @@ pytestmark = pytest.mark.skipif(not os.path.exists(sv.lib_path()), reason="libsp
 FAKE = 0x10000  # never dereferenced: the calls below fail host checks or have nothing to do
 
 
+class PagedCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "heads", "head_dim", "page_size", "num_pages", "max_pages")]
+                + [("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                   ("v", ctypes.c_void_p)]
+                + [(f"{kv}_{n}_stride", ctypes.c_int64) for kv in "kv" for n in ("page", "token", "head")]
+                + [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)])
+
+
 def text():
     return re.sub(r"/\*.*?\*/", " ", open(HEADER).read(), flags=re.S)
 
@@ -52,11 +60,14 @@ def test_binding_signatures_match_header_prototypes():
 
 def test_cache_struct_matches_header():
     body = re.search(r"typedef struct \{(.*?)\} sv_paged_cache;", text(), re.S).group(1)
+    letters = {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P"}
     fields = []
     for decl in filter(None, (" ".join(d.split()) for d in body.split(";"))):
         kind, names = re.match(r"((?:const )?\w+\s?\*?)\s*(.*)", decl).groups()
         fields += [(n.strip(), ctype_of(kind)) for n in names.split(",")]
-    assert fields == attn._PagedCache._fields_
+    assert fields == PagedCache._fields_
+    packed = re.sub(r"(\d+)(\w)", lambda m: m.group(2) * int(m.group(1)), attn._CACHE.format.lstrip("@"))
+    assert packed == "".join(letters[t] for _, t in fields) and attn._CACHE.size == ctypes.sizeof(PagedCache)
 
 
 def test_header_constants_match_binding():
@@ -126,7 +137,7 @@ def cache(**kw):
     a = dict(dtype=1, heads=2, head_dim=64, page_size=16, num_pages=5, max_pages=3, page_table=FAKE, page_table_stride=3,
              k=FAKE, v=FAKE, k_page_stride=2048, k_token_stride=128, k_head_stride=64, v_page_stride=2048,
              v_token_stride=128, v_head_stride=64, k_scale=None, v_scale=None)
-    return attn._PagedCache(**{**a, **kw})
+    return PagedCache(**{**a, **kw})
 
 
 BAD_CACHES = [

@@ -220,17 +220,15 @@ def test_gather_matches_the_oracle(cache, order, dtype, lengths, begin, page, he
 
 def test_gather_of_one_of_the_two():
     """The C call with one output missing writes the other alone."""
-    import ctypes
-
     from draft_token_verification_spec_amd import attn
 
     c = new_cache("bf16", 2, 8, 1, 16)
     c["v_cache"].copy_(torch.randn((2, 8, 1, 16)))
-    dev = torch.device("cuda", torch.cuda.current_device())
+    dev = torch.cuda.current_device()
     table, start = I32([[1]]), I32([0, 5])
-    p = attn._paged(dev, 1, c["k_cache"], c["v_cache"], table, None, None)
+    p = attn._paged(dev, 1, c["k_cache"], c["v_cache"], table, None, None)[0]
     out = torch.zeros((5, 1, 16), device="cuda")
-    attn._call(dev, "sv_kv_gather", 1, 5, sv.SV_F32, ctypes.addressof(p), start.data_ptr(), None, None, out.data_ptr())
+    attn._call(dev, "sv_kv_gather", 1, 5, sv.SV_F32, p, start.data_ptr(), None, None, out.data_ptr())
     assert torch.equal(out, c["v_cache"][1, :5].float())
 
 
