@@ -37,53 +37,60 @@ constexpr int kBlock = 32;  // tokens a wave takes at a time
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// One tile of rows of one request, as every kernel sees it.
+// Values that every lane of a workgroup reads alike (lengths, page tables) go
+// through the scalar cache: a vector load would wait behind the streamed keys
+// and values of the compute unit.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int32_t uniform_at(const int32_t* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) int32_t*)(p))[i];
+}
+
+// 16 bytes at a scalar address plus a lane's 32-bit offset.  The offset is made
+// opaque here so that the load takes both as they are, instead of a 64-bit
+// vector address formed ahead and kept in registers.
+__device__ __forceinline__ uint4 load_from(const char* p, uint32_t at) {
+  asm volatile("" : "+v"(at));
+  return *reinterpret_cast<const uint4*>(p + at);
+}
+
+// One tile of rows of one request.
 struct Tile {
-  int b, first_row;      // request, tile's first row in it (row = token * G + head in group)
-  int rows;              // rows of the tile, <= kRowTile; 0: nothing to do
-  int token0;            // the request's first packed row
-  int place0;            // place of the request's first new token
-  int begin, end;        // tokens that some row of the tile may see
-  int held;              // tokens of the request in the cache
+  int first_row;   // tile's first row in the request (row = token * G + head in group)
+  int rows;        // rows of the tile; 0: nothing to do
+  int token0;      // the request's first packed row
+  int place0;      // place of the request's first new token
+  int begin, end;  // tokens that some row of the tile may see
 };
 
-// Slot `slot` of the launch: the tiles of request b take the slots from
-// query_start[b] * G / kRowTile + b on, which leaves room for all of them
-// (ceil(n G / M) <= floor((s + n) G / M) - floor(s G / M) + 1) and grows
-// strictly with b.  By the whole wave.
+// The tile of request b whose first row is first_row; rows == 0 beyond the
+// request's last.
 template <int M>
-__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int G, int slot, int lane) {
+__device__ __forceinline__ Tile tile_at(const AttnArgs& a, int G, int b, int64_t first_row) {
   Tile t;
   t.rows = 0;
-  int lo = 0, hi = a.B;
-  auto first_slot = [&](int b) { return int64_t(a.query_start[b]) * G / M + b; };
-  while (lo < hi) {
-    const int step = (hi - lo + 63) >> 6;
-    const int at = lo + lane * step;
-    const bool in = at < hi;
-    const int n = __popcll(__ballot(in && first_slot(in ? at : lo) <= slot));
-    if (n == 0) break;
-    const int base = lo;
-    lo = base + (n - 1) * step + 1;
-    hi = min(hi, base + n * step);
-  }
-  t.b = lo - 1;
-  if (t.b < 0) return t;
-  t.token0 = a.query_start[t.b];
-  const int64_t n = int64_t(a.query_start[t.b + 1]) - t.token0;
-  const int64_t first = (slot - first_slot(t.b)) * M;
-  const int64_t rows = n * G - first;
+  t.token0 = uniform_at(a.query_start, b);
+  const int64_t n = int64_t(uniform_at(a.query_start, b + 1)) - t.token0;
+  const int64_t rows = n * G - first_row;
   if (t.token0 < 0 || int64_t(t.token0) + n > a.T || rows <= 0) return t;
-  t.first_row = int(first);
+  t.first_row = int(first_row);
   t.rows = int(min(rows, int64_t(M)));
-  const int64_t len = max(a.kv_len[t.b], 0);
-  t.held = int(max(int64_t(0), min(len, int64_t(a.cache.max_pages) << a.cache.page_shift)));
+  const int64_t len = max(uniform_at(a.kv_len, b), 0);
+  const int64_t held = min(len, int64_t(a.cache.max_pages) << a.cache.page_shift);
   const int64_t place0 = len - n;
   t.place0 = int(place0);
-  const int64_t first_place = place0 + first / G, last_place = place0 + (first + t.rows - 1) / G;
-  t.end = int(max(int64_t(0), min(int64_t(t.held), last_place + 1)));
+  const int64_t first_place = place0 + t.first_row / G, last_place = place0 + (t.first_row + t.rows - 1) / G;
+  t.end = int(max(int64_t(0), min(held, last_place + 1)));
   t.begin = a.window > 0 ? int(min(int64_t(t.end), max(int64_t(0), first_place - a.window + 1))) : 0;
+  // 64-bit comparisons are vector instructions: back to scalars
+  t.token0 = uniform(t.token0), t.rows = uniform(t.rows), t.first_row = uniform(t.first_row);
+  t.place0 = uniform(t.place0), t.begin = uniform(t.begin), t.end = uniform(t.end);
   return t;
+}
+
+// Byte offset of a page's token in keys or values: strides in units of 16 bytes.
+__device__ __forceinline__ uint64_t row_at(const UnitStrides& u, int page, int slot, int head) {
+  return ((uint64_t(uint32_t(page)) * u.page + uint64_t(uint32_t(slot)) * u.token) + uint64_t(uint32_t(head)) * u.head)
+         << 4;
 }
 
 // The splits that have tokens of [begin, end): first .. last (empty: 0 .. 0).
@@ -95,11 +102,11 @@ __device__ __forceinline__ Splits live_splits(const Tile& t, int split_len, int 
   return {min(t.begin / split_len, num_splits - 1), min((t.end - 1) / split_len, num_splits - 1)};
 }
 
-__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {  // either packed bf16 is infinite or NaN
-  return ((w & 0x7f80u) == 0x7f80u) | ((w & 0x7f800000u) == 0x7f800000u);
-}
-__device__ __forceinline__ bool not_finite8(const uint4& w) {
-  return (not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w)) != 0;
+// Bits 15 and 31 tell whether a packed bf16 is infinite or NaN (an exponent of
+// ones carries into its sign).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t not_finite8(const uint4& w) {
+  return (not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w)) & 0x80008000u;
 }
 
 __device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, const f32x4& c) {
@@ -115,49 +122,59 @@ __device__ __forceinline__ uint2 read_transposed(const uint16_t* p) {
   return __builtin_bit_cast(uint2, r);
 }
 
-// Where element e of a value row lies in LDS: rows of DP elements, their
-// 32-byte units permuted by the row so that the rows that one transposing read
-// takes (and one store writes) fall on different banks.
+// Elements between rows in LDS.  The 16 bytes beyond a row of keys set
+// successive rows off by one 16-byte unit, so that 8 rows' units of the same
+// channels (a load of the A operand) lie on different banks; a transposing read
+// takes 32 bytes of 4 rows at a time, which 32 bytes beyond a row keep apart.
+// (The few-rows kernel stores its values 16 rows at a time, for which 16 bytes
+// are as good on balance.)  The addresses stay sums, whose constant parts are
+// the instructions' offsets.
 template <int DP>
-__device__ __forceinline__ int value_at(int row, int e) {
-  const int flip = DP == 64 ? (row >> 1) & 3 : row & 7;
-  return row * DP + (e ^ (flip << 4));
-}
+constexpr int kPitch = DP + 8;
+template <int DP>
+constexpr int kValuePitch = DP + 16;
 
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
 
-template <int DP, int MT, bool FP8>
-__global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) void few_rows_kernel(AttnArgs a, AttnPlan p) {
+// SMALL: pages of fewer than 16 tokens (or rows too far apart for a 32-bit
+// offset within 16 tokens): every lane looks its token's page up.  Otherwise 16
+// tokens lie in one page, whose address is scalar.
+template <int DP, int MT, bool FP8, bool SMALL>
+__global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP * MT >= 128 ? 2 : 3) void few_rows_kernel(
+    AttnArgs a, AttnPlan p) {
   constexpr int M = 16 * MT;
   constexpr int kSteps = DP / 32;        // of the score product
   constexpr int kDT = DP / 16;           // channel tiles of the result
   constexpr int kLoads = FP8 ? DP / 64 : DP / 32;  // 16-byte loads of a token's row per lane
-  __shared__ __align__(16) uint16_t values[kAttnWaves][kBlock * DP];
+  __shared__ __align__(16) uint16_t values[kAttnWaves][kBlock * kPitch<DP>];
   __shared__ float stat_m[kAttnWaves][M], stat_l[kAttnWaves][M];
 
-  const PagedView& c = a.cache;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const CacheView& c = a.cache;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int G = a.q_heads / c.heads;
-  const Tile t = find_tile<M>(a, G, blockIdx.x, lane);
+  const int b = blockIdx.x / p.tiles;
+  for (int64_t first_row = int64_t(blockIdx.x - b * p.tiles) * M;; first_row += int64_t(p.tiles) * M) {
+  const Tile t = tile_at<M>(a, G, b, first_row);
   if (t.rows == 0) return;
   const Splits live = live_splits(t, p.split_len, p.num_splits);
-  if (split < live.first || split > live.last) return;
+  if (split < live.first || split > live.last) continue;
   const int begin = max(t.begin, split * p.split_len) & ~(kBlock - 1);
-  const int end = split == p.num_splits - 1 ? t.end : min(int64_t(t.end), int64_t(split + 1) * p.split_len);
+  const int end = split == p.num_splits - 1 ? t.end : min(t.end, (split + 1) * p.split_len);
 
   // queries: the B operand, lane (row, g) holding the channels of its steps
   const int chunks = c.D >> 3;
   uint4 qf[MT][kSteps];
-  int place[MT];
+  int place[MT], oldest[MT];  // of the lane's rows: they see the tokens oldest < j <= place
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
     const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
     place[m] = row < t.rows ? t.place0 + tok : -1;
+    oldest[m] = a.window > 0 ? max(place[m], -1) - a.window : -1;
     const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -183,30 +200,44 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
   uint4 kr[2][kLoads], vr[2][kLoads];
   uint32_t ks[2] = {127, 127}, vs[2] = {127, 127};
   bool have[2];
-  // the pages of the block's tokens r and 16 + r (-1: absent)
+  const int64_t table = b * c.table_stride;
+  const int in_page = (1 << c.page_shift) - 1;
+  // the page table's entries of the block's tokens 0 .. 15 and 16 .. 31 (SMALL:
+  // of this lane's, r and 16 + r), or of the last token in their place
   auto pages = [&](int base, int (&page)[2]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) page[h] = base < end ? page_of(c, t.b, base + 16 * h + r) : -1;
+    for (int h = 0; h < 2; ++h) {
+      const int j = min(base + 16 * h + (SMALL ? r : 0), end - 1);
+      page[h] = SMALL ? c.table[table + (j >> c.page_shift)] : uniform_at(c.table, table + (j >> c.page_shift));
+    }
   };
   // ask for a block's rows; the loads of absent tokens and of channels beyond
   // the head's go to page 0 and to its last channels, and are not used
+  uint32_t lane_at[2][kLoads];  // bytes from the 16 tokens' first row, of keys and of values
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const uint32_t unit = min(4 * i + g, (FP8 ? c.D >> 4 : c.D >> 3) - 1);
+    lane_at[0][i] = (uint32_t(SMALL ? 0 : r) * c.ku.token + unit) << 4;
+    lane_at[1][i] = (uint32_t(SMALL ? 0 : r) * c.vu.token + unit) << 4;
+  }
   auto request = [&](int base, const int (&page)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = max(page[h], 0), slot = (base + 16 * h + r) & ((1 << c.page_shift) - 1);
-      have[h] = page[h] >= 0 && base + 16 * h + r < end;
-      const int64_t ko = at * c.k_page + slot * c.k_token + kvh * c.k_head;
-      const int64_t vo = at * c.v_page + slot * c.v_token + kvh * c.v_head;
+      const int j = base + 16 * h + (SMALL ? r : 0);
+      const bool found = uint32_t(page[h]) < uint32_t(c.num_pages);
+      const int at = found ? page[h] : 0, slot = j & in_page;
+      have[h] = found && j + (SMALL ? 0 : r) < end;
+      const char* kp = static_cast<const char*>(c.k) + row_at(c.ku, at, slot, kvh);
+      const char* vp = static_cast<const char*>(c.v) + row_at(c.vu, at, slot, kvh);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int unit = min(4 * i + g, (FP8 ? c.D >> 4 : c.D >> 3) - 1);  // of 16 bytes
-        kr[h][i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.k) + (FP8 ? ko : 2 * ko) + 16 * unit);
-        vr[h][i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.v) + (FP8 ? vo : 2 * vo) + 16 * unit);
+        kr[h][i] = load_from(kp, lane_at[0][i]);
+        vr[h][i] = load_from(vp, lane_at[1][i]);
       }
       if (FP8) {
         const int64_t so = ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot;
-        ks[h] = c.k_scale[so];
-        vs[h] = c.v_scale[so];
+        ks[h] = c.k_scale[so + (SMALL ? 0 : r)];
+        vs[h] = c.v_scale[so + (SMALL ? 0 : r)];
       }
     }
   };
@@ -214,9 +245,11 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
   const int stride = kAttnWaves * kBlock;
   int base = begin + wave * kBlock;
   int page[2];
-  pages(base, page);
-  if (base < end) request(base, page);
-  pages(base + stride, page);
+  if (base < end) {
+    pages(base, page);
+    request(base, page);
+    pages(base + stride, page);
+  }
   uint16_t* const mine = values[wave];
   for (; base < end; base += stride) {
     // S^T, a block's 16 tokens by 16 rows at a time
@@ -246,38 +279,38 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
     uint32_t hidden = 0, nan = 0;  // bit 16 h + i: token 16 h + i is absent; its value is not finite
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint4 w[kLoads * (FP8 ? 2 : 1)];
-      if (FP8) {
-        const float vscale = scale_of(vs[h]);
+      uint16_t* const to = mine + (16 * h + r) * kPitch<DP> + (FP8 ? 16 : 8) * g;
+      uint32_t bad = 0;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          w[2 * i] = dequant8(make_uint2(vr[h][i].x, vr[h][i].y), vscale);
-          w[2 * i + 1] = dequant8(make_uint2(vr[h][i].z, vr[h][i].w), vscale);
+      for (int i = 0; i < kLoads; ++i) {
+        if (FP8) {
+          const float vscale = scale_of(vs[h]);
+          const uint4 lo = dequant8(make_uint2(vr[h][i].x, vr[h][i].y), vscale);
+          const uint4 hi = dequant8(make_uint2(vr[h][i].z, vr[h][i].w), vscale);
+          *reinterpret_cast<uint4*>(to + 64 * i) = lo;
+          *reinterpret_cast<uint4*>(to + 64 * i + 8) = hi;
+          if (!whole) bad |= not_finite8(lo) | not_finite8(hi);
+        } else {
+          *reinterpret_cast<uint4*>(to + 32 * i) = vr[h][i];
+          if (!whole) bad |= not_finite8(vr[h][i]);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) w[i] = vr[h][i];
       }
       if (!whole) {
         // a weight of zero does not stop a value that is not finite: such
         // values are taken out, and their tokens' scores made NaN instead
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < kLoads * (FP8 ? 2 : 1); ++i) bad |= not_finite8(w[i]);
-        uint64_t any = __ballot(bad && have[h]);
+        uint64_t any = __ballot(bad != 0 && have[h]);
         any |= any >> 32;
         any |= any >> 16;
         nan |= uint32_t(any & 0xffffu) << (16 * h);
         hidden |= uint32_t(~__ballot(have[h]) & 0xffffu) << (16 * h);
-        const bool drop = !have[h] || ((any >> r) & 1u);
+        asm volatile("" ::: "memory");  // (a store of its own: else every value would be chosen in registers first)
+        if (!have[h] || ((any >> r) & 1u)) {
 #pragma unroll
-        for (int i = 0; i < kLoads * (FP8 ? 2 : 1); ++i)
-          if (drop) w[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < kLoads * (FP8 ? 2 : 1); ++i) {
-        const int ch = FP8 ? 8 * (i >> 1) + 2 * g + (i & 1) : 4 * i + g;
-        *reinterpret_cast<uint4*>(mine + value_at<DP>(16 * h + r, 8 * ch)) = w[i];
+          for (int i = 0; i < kLoads; ++i) {
+            *reinterpret_cast<uint4*>(to + (FP8 ? 64 : 32) * i) = make_uint4(0u, 0u, 0u, 0u);
+            if (FP8) *reinterpret_cast<uint4*>(to + 64 * i + 8) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
       }
     }
     const int now = base;
@@ -294,8 +327,9 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
           const bool off = (hidden >> k) & 1u, bad = (nan >> k) & 1u;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const bool sees = !off && j <= place[m] && (a.window == 0 || j > place[m] - a.window);
-            s[h][m][i] = sees ? (bad ? NAN : s[h][m][i]) : -INFINITY;
+            const bool sees = !off & (j <= place[m]) & (j > oldest[m]);
+            const float x = bad ? NAN : s[h][m][i];
+            s[h][m][i] = sees ? x : -INFINITY;
           }
         }
     }
@@ -329,11 +363,11 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
 #pragma unroll
       for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
     }
+    const uint16_t* const vt = mine + (4 * g + (r >> 2)) * kPitch<DP> + 4 * (r & 3);
 #pragma unroll
     for (int d = 0; d < kDT; ++d) {
-      const int e = 16 * d + 4 * (r & 3);
-      const uint2 v0 = read_transposed(mine + value_at<DP>(4 * g + (r >> 2), e));
-      const uint2 v1 = read_transposed(mine + value_at<DP>(16 + 4 * g + (r >> 2), e));
+      const uint2 v0 = read_transposed(vt + 16 * d);
+      const uint2 v1 = read_transposed(vt + 16 * kPitch<DP> + 16 * d);
       const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
 #pragma unroll
       for (int m = 0; m < MT; ++m) o[d][m] = mfma16(vf, pf[m], o[d][m]);
@@ -352,6 +386,8 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
   }
   __syncthreads();
   const bool alone = live.first == live.last;
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // (what follows from it is formed here, not kept in registers through the loop)
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
@@ -367,7 +403,7 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
       for (int i = 0; i < 4; ++i) part[(16 * d + 4 * g + i) * 16 + r] = o[d][m][i] * keep;
     __syncthreads();
     // 16 rows by 16 threads, 8 channels at a time
-    const int orow = threadIdx.x & 15;
+    const int orow = tid & 15;
     const int trow = 16 * m + orow;
     if (trow < t.rows) {
       float rtop = -INFINITY, total = 0.f;
@@ -379,7 +415,7 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
       const int tok = t.token0 + (t.first_row + trow) / G, head = kvh * G + (t.first_row + trow) % G;
       const int64_t at = int64_t(tok) * a.q_heads + head;
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      for (int ch = threadIdx.x >> 4; ch < chunks; ch += 16) {
+      for (int ch = tid >> 4; ch < chunks; ch += 16) {
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -394,7 +430,7 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
         else
           store8(p.part_o + (split * (int64_t(a.T) * a.q_heads) + at) * c.D + 8 * ch, y);
       }
-      if (threadIdx.x < 16) {
+      if (tid < 16) {
         if (!alone)
           p.part_ml[split * (int64_t(a.T) * a.q_heads) + at] = make_float2(rtop == -INFINITY ? rtop : rref, total);
         else if (a.lse)
@@ -402,6 +438,7 @@ __global__ __launch_bounds__(kAttnThreads, MT >= 4 || DP * MT > 256 ? 1 : 2) voi
       }
     }
     __syncthreads();
+  }
   }
 }
 
@@ -416,18 +453,10 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, const f
                                                  0);
 }
 
-// Where element e of a key row lies in LDS: 16-byte units permuted by the row
-// so that 16 rows' units of the same channels fall on different banks.
-template <int DP>
-__device__ __forceinline__ int key_at(int row, int e) {
-  const int flip = DP == 64 ? (row >> 1) & 7 : row & 15;
-  return row * DP + (e ^ (flip << 3));
-}
-
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kManyRows = 32 * kAttnWaves;
 
-template <int DP, bool FP8>
+template <int DP, bool FP8, bool SMALL>
 __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kernel(AttnArgs a, AttnPlan p) {
   constexpr int M = kManyRows;
   constexpr int kSteps = DP / 16;
@@ -436,28 +465,40 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
   constexpr int kSpan = kAttnThreads / kLanes;        // tokens of one load of the workgroup
   constexpr int kLoads = kTile / kSpan;
   constexpr int kParts = FP8 ? 2 : 1;                 // 8 channels each, of a load
-  __shared__ __align__(16) uint16_t keys[2][kTile * DP];
-  __shared__ __align__(16) uint16_t values[2][kTile * DP];
+  __shared__ __align__(16) uint16_t keys[2][kTile * kPitch<DP>];
+  __shared__ __align__(16) uint16_t values[2][kTile * kValuePitch<DP>];
   __shared__ __align__(16) uint8_t state[2][kTile];   // of a token: 0 present, 1 absent, 2 a value not finite
   __shared__ __align__(16) int lacks[2][kAttnWaves];  // some token that this wave loaded is absent
 
-  const PagedView& c = a.cache;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const CacheView& c = a.cache;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int split = blockIdx.z;
   const int G = a.q_heads / c.heads;
+  // workgroups go to the 8 XCDs in turn: each takes whole heads, whose keys and
+  // values then pass through one L2 only
+  uint32_t at_x = blockIdx.x, kvh = blockIdx.y;
+  if ((c.heads & 7) == 0) {
+    const uint32_t i = blockIdx.x + blockIdx.y * gridDim.x, per = gridDim.x * (c.heads >> 3);
+    const uint32_t pos = (i & 7) * per + (i >> 3);
+    kvh = pos / gridDim.x;
+    at_x = pos - kvh * gridDim.x;
+  }
+  const int b = at_x / p.tiles;
   // later tiles of a prompt see more: they start first
-  const Tile t = find_tile<M>(a, G, gridDim.x - 1 - blockIdx.x, lane);
+  for (int64_t first_row = int64_t(p.tiles - 1 - (at_x - b * p.tiles)) * M;; first_row += int64_t(p.tiles) * M) {
+  const Tile t = tile_at<M>(a, G, b, first_row);
   if (t.rows == 0) return;
   const Splits live = live_splits(t, p.split_len, p.num_splits);
-  if (split < live.first || split > live.last) return;
+  if (split < live.first || split > live.last) continue;
   const int begin = max(t.begin, split * p.split_len) & ~(kTile - 1);
-  const int end = split == p.num_splits - 1 ? t.end : min(int64_t(t.end), int64_t(split + 1) * p.split_len);
+  const int end = split == p.num_splits - 1 ? t.end : min(t.end, (split + 1) * p.split_len);
 
   const int chunks = c.D >> 3;
   const int row = 32 * wave + r;
   const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
   const int place = row < t.rows ? t.place0 + tok : -1;
+  const int oldest = a.window > 0 ? max(place, -1) - a.window : -1;  // the row sees the tokens oldest < j <= place
   uint4 qf[kSteps];
   {
     const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
@@ -481,34 +522,44 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float mx = -INFINITY, l = 0.f;
 
-  // staging: thread -> token kSpan * i + tid / kLanes, 16 bytes tid % kLanes
-  const int unit = min(tid % kLanes, (FP8 ? c.D >> 4 : chunks) - 1);
+  // staging: thread -> token kSpan * i + tid / kLanes, 16 bytes tid % kLanes;
+  // a wave's kWaveSpan tokens of a load lie in one page unless SMALL
+  constexpr int kWaveSpan = 64 / kLanes;
   uint4 kr[kLoads], vr[kLoads];
   uint32_t ks[kLoads], vs[kLoads];
   int page[kLoads];
+  const int64_t table = b * c.table_stride;
+  const int in_page = (1 << c.page_shift) - 1;
+  const int own = SMALL ? tid / kLanes : wave * kWaveSpan;  // of a load's tokens, the first that `page` is of
+  const int from = SMALL ? 0 : lane / kLanes;               // this thread's token behind it
   auto pages = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int j = base + kSpan * i + tid / kLanes;
-      page[i] = j < end ? page_of(c, t.b, j) : -1;
+      const int j = min(base + kSpan * i + own, end - 1);
+      page[i] = SMALL ? c.table[table + (j >> c.page_shift)] : uniform_at(c.table, table + (j >> c.page_shift));
     }
   };
+  uint32_t lane_at[2];  // bytes from that token's row
+  {
+    const uint32_t unit = min(tid % kLanes, (FP8 ? c.D >> 4 : chunks) - 1);
+    lane_at[0] = (uint32_t(from) * c.ku.token + unit) << 4;
+    lane_at[1] = (uint32_t(from) * c.vu.token + unit) << 4;
+  }
   uint32_t absent;  // bit i: load i's token is absent
   auto request = [&](int base) {
     absent = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int j = base + kSpan * i + tid / kLanes;
-      absent |= uint32_t(page[i] < 0) << i;
-      const int at = max(page[i], 0), slot = j & ((1 << c.page_shift) - 1);
-      const int64_t ko = at * c.k_page + slot * c.k_token + kvh * c.k_head;
-      const int64_t vo = at * c.v_page + slot * c.v_token + kvh * c.v_head;
-      kr[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.k) + (FP8 ? ko : 2 * ko) + 16 * unit);
-      vr[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.v) + (FP8 ? vo : 2 * vo) + 16 * unit);
+      const int j = base + kSpan * i + own;
+      const bool found = uint32_t(page[i]) < uint32_t(c.num_pages);
+      absent |= uint32_t(!found || j + from >= end) << i;
+      const int at = found ? page[i] : 0, slot = j & in_page;
+      kr[i] = load_from(static_cast<const char*>(c.k) + row_at(c.ku, at, slot, kvh), lane_at[0]);
+      vr[i] = load_from(static_cast<const char*>(c.v) + row_at(c.vu, at, slot, kvh), lane_at[1]);
       if (FP8) {
         const int64_t so = ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot;
-        ks[i] = c.k_scale[so];
-        vs[i] = c.v_scale[so];
+        ks[i] = c.k_scale[so + from];
+        vs[i] = c.v_scale[so + from];
       }
     }
   };
@@ -537,7 +588,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
         // a weight of zero does not stop a value that is not finite: such
         // values are taken out, and their tokens' scores made NaN instead
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) bad |= not_finite8(vw[q]);
+        for (int q = 0; q < kParts; ++q) bad |= not_finite8(vw[q]) != 0;
         const uint64_t any = __ballot(bad && !gone);
         bad = (any >> (lane & ~(kLanes - 1))) & ((uint64_t(1) << kLanes) - 1);
       }
@@ -548,8 +599,8 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
 #pragma unroll
       for (int q = 0; q < kParts; ++q) {
         const int e = 8 * (kParts * (tid % kLanes) + q);
-        *reinterpret_cast<uint4*>(&keys[buf][key_at<DP>(at, e)]) = kw[q];
-        *reinterpret_cast<uint4*>(&values[buf][value_at<DP>(at, e)]) = vw[q];
+        *reinterpret_cast<uint4*>(&keys[buf][at * kPitch<DP> + e]) = kw[q];
+        *reinterpret_cast<uint4*>(&values[buf][at * kValuePitch<DP> + e]) = vw[q];
       }
       if (tid % kLanes == 0) state[buf][at] = gone ? 1 : bad ? 2 : 0;
     }
@@ -558,8 +609,8 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
   };
 
   int buf = 0;
-  pages(begin);
   if (begin < end) {
+    pages(begin);
     request(begin);
     pages(begin + kTile);
     stage(begin, 0);
@@ -567,15 +618,12 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
   __syncthreads();
   for (int base = begin; base < end; base += kTile) {
     const bool more = base + kTile < end;
-    if (more) {
-      request(base + kTile);
-      pages(base + 2 * kTile);
-    }
+    if (more) request(base + kTile);
     // a wave whose rows see nothing here only helps to load
-    if (base <= wave_last && (a.window == 0 || base + kTile - 1 > wave_first - a.window)) {
-      const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
-      const bool masked = !whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0;
-      f32x16 s[2];
+    const bool sees_some = base <= wave_last && (a.window == 0 || base + kTile - 1 > wave_first - a.window);
+    f32x16 s[2];
+    if (sees_some) {
+      const uint16_t* const kt = &keys[buf][r * kPitch<DP> + 8 * h];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -584,9 +632,16 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
       for (int st = 0; st < kSteps; ++st)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint4 kf = *reinterpret_cast<const uint4*>(&keys[buf][key_at<DP>(32 * u + r, 8 * (2 * st + h))]);
+          const uint4 kf = *reinterpret_cast<const uint4*>(kt + 32 * u * kPitch<DP> + 16 * st);
           s[u] = mfma32(kf, qf[st], s[u]);
         }
+    }
+    // (here, ahead of the softmax: a scalar load in flight holds up LDS reads)
+    if (more) pages(base + 2 * kTile);
+    if (sees_some) {
+      const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
+      const bool masked = !whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0;
+      const uint16_t* const vt = &values[buf][(4 * h + ((lane & 15) >> 2)) * kValuePitch<DP> + (lane & 16) + 4 * (lane & 3)];
       if (masked) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -597,8 +652,9 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
             for (int i = 0; i < 4; ++i) {
               const int j = base + 32 * u + 8 * k + 4 * h + i;
               const uint32_t is = (w >> (8 * i)) & 0xffu;
-              const bool sees = is != 1 && j <= place && (a.window == 0 || j > place - a.window);
-              s[u][4 * k + i] = sees ? (is == 2 ? NAN : s[u][4 * k + i]) : -INFINITY;
+              const bool sees = (is != 1) & (j <= place) & (j > oldest);
+              const float x = is == 2 ? NAN : s[u][4 * k + i];
+              s[u][4 * k + i] = sees ? x : -INFINITY;
             }
           }
       }
@@ -632,12 +688,10 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
           const uint4 pf = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
                                       pack_bf16(s[u][8 * q + 4], s[u][8 * q + 5]),
                                       pack_bf16(s[u][8 * q + 6], s[u][8 * q + 7]));
-          const int at = 32 * u + 16 * q + 4 * h + ((lane & 15) >> 2);
 #pragma unroll
           for (int d = 0; d < kDT; ++d) {
-            const int e = 32 * d + (lane & 16) + 4 * (lane & 3);
-            const uint2 v0 = read_transposed(&values[buf][value_at<DP>(at, e)]);
-            const uint2 v1 = read_transposed(&values[buf][value_at<DP>(at + 8, e)]);
+            const uint2 v0 = read_transposed(vt + (32 * u + 16 * q) * kValuePitch<DP> + 32 * d);
+            const uint2 v1 = read_transposed(vt + (32 * u + 16 * q + 8) * kValuePitch<DP> + 32 * d);
             o[d] = mfma32(make_uint4(v0.x, v0.y, v1.x, v1.y), pf, o[d]);
           }
         }
@@ -648,7 +702,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
   }
 
   l += __shfl_xor(l, 32, 64);
-  if (row >= t.rows) return;
+  if (row >= t.rows) continue;  // (the barriers above have ended every wave's reads of LDS)
   const float ref = mx == -INFINITY ? 0.f : mx * sc;
   const int64_t at = int64_t(t.token0 + tok) * a.q_heads + head;
   if (live.first == live.last) {
@@ -677,6 +731,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
       }
     if (h == 0) p.part_ml[part] = make_float2(mx == -INFINITY ? mx : ref, l);
   }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -687,7 +742,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
 // weight, then the weighted values are summed, four channels a lane.
 template <int M>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan p) {
-  const PagedView& c = a.cache;
+  const CacheView& c = a.cache;
   const int lane = threadIdx.x & 63;
   const int64_t at = int64_t(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
   const int64_t all = int64_t(a.T) * a.q_heads;
@@ -698,7 +753,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan
   if (b < 0 || tok >= a.query_start[b + 1]) return;
   // the row's tile, as the kernel that wrote the parts saw it
   const int64_t row = int64_t(tok - a.query_start[b]) * G + head % G;
-  const Tile t = find_tile<M>(a, G, int(int64_t(a.query_start[b]) * G / M + b + row / M), lane);
+  const Tile t = tile_at<M>(a, G, uniform(b), uniform(int(row / M)) * int64_t(M));
   if (t.rows == 0) return;
   const Splits live = live_splits(t, p.split_len, p.num_splits);
   if (live.first == live.last) return;  // written by the split itself
@@ -731,26 +786,35 @@ void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   hipLaunchKernelGGL(join_kernel<M>, grid, block, 0, stream, a, p);
 }
 
-template <int DP, int MT, bool FP8>
+template <int DP, int MT, bool FP8, bool SMALL>
 void launch_few(const AttnArgs& a, const AttnPlan& p, const dim3& grid, hipStream_t stream) {
-  hipLaunchKernelGGL((few_rows_kernel<DP, MT, FP8>), grid, dim3(kAttnThreads), 0, stream, a, p);
+  hipLaunchKernelGGL((few_rows_kernel<DP, MT, FP8, SMALL>), grid, dim3(kAttnThreads), 0, stream, a, p);
   launch_join<16 * MT>(a, p, stream);
 }
 
-template <int DP, bool FP8>
+template <int DP, bool FP8, bool SMALL>
 void launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  const int64_t G = a.q_heads / a.cache.heads;
-  const dim3 grid(a.T * G / p.row_tile + a.B, a.cache.heads, p.num_splits);
+  const dim3 grid(a.B * p.tiles, a.cache.heads, p.num_splits);
   if (p.row_tile == 16) {
-    launch_few<DP, 1, FP8>(a, p, grid, stream);
+    launch_few<DP, 1, FP8, SMALL>(a, p, grid, stream);
   } else if (p.row_tile == 32) {
-    launch_few<DP, 2, FP8>(a, p, grid, stream);
+    launch_few<DP, 2, FP8, SMALL>(a, p, grid, stream);
   } else if (p.row_tile == kManyRows) {
-    hipLaunchKernelGGL((many_rows_kernel<DP, FP8>), grid, dim3(kAttnThreads), 0, stream, a, p);
+    hipLaunchKernelGGL((many_rows_kernel<DP, FP8, SMALL>), grid, dim3(kAttnThreads), 0, stream, a, p);
     launch_join<kManyRows>(a, p, stream);
   } else if constexpr (DP < 256) {
-    launch_few<DP, 4, FP8>(a, p, grid, stream);
+    launch_few<DP, 4, FP8, SMALL>(a, p, grid, stream);
   }
+}
+
+template <bool FP8, bool SMALL>
+void launch_dims(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  if (a.cache.D <= 64)
+    launch_rows<64, FP8, SMALL>(a, p, stream);
+  else if (a.cache.D <= 128)
+    launch_rows<128, FP8, SMALL>(a, p, stream);
+  else
+    launch_rows<256, FP8, SMALL>(a, p, stream);
 }
 
 }  // namespace
@@ -761,12 +825,18 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   if (max_q_len <= 0 || max_q_len > T) max_q_len = B > 0 ? (T + B - 1) / B : T;
   const int64_t rows = int64_t(max_q_len) * G;
   p.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && D <= 128 ? 64 : kManyRows;
+  // a request's tiles, as far as known; workgroups go on to further ones where
+  // a request has more
+  int64_t tiles = (rows + p.row_tile - 1) / p.row_tile;
+  const int64_t most_tiles = (1 << 20) / (B > 0 ? B : 1);  // (tiles of all requests and heads: 32 bits)
+  tiles = tiles < most_tiles ? tiles : most_tiles;
+  p.tiles = int(tiles < 1 ? 1 : tiles);
   // enough workgroups for every compute unit several times over, of at least
   // 256 tokens each
-  const int64_t tiles = (int64_t(T) * G / p.row_tile + (B < T ? B : T)) * kv_heads;
+  const int64_t groups = int64_t(B) * p.tiles * kv_heads;
   const int64_t most = (int64_t(max_kv_len) + 255) / 256;
   const int64_t want = p.row_tile == kManyRows ? 512 : 2048;
-  int64_t n = tiles > 0 ? (want + tiles - 1) / tiles : 1;
+  int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
   n = n < most ? n : most;
   n = n < 1 ? 1 : n;
   int64_t len = (max_kv_len + n - 1) / n;
@@ -783,21 +853,12 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
 }
 
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream) {
-  if (cache_dtype == SV_E4M3) {
-    if (a.cache.D <= 64)
-      launch_rows<64, true>(a, p, stream);
-    else if (a.cache.D <= 128)
-      launch_rows<128, true>(a, p, stream);
-    else
-      launch_rows<256, true>(a, p, stream);
-  } else {
-    if (a.cache.D <= 64)
-      launch_rows<64, false>(a, p, stream);
-    else if (a.cache.D <= 128)
-      launch_rows<128, false>(a, p, stream);
-    else
-      launch_rows<256, false>(a, p, stream);
-  }
+  const auto near = [](const UnitStrides& u) { return u.token < (uint32_t(1) << 24); };  // 16 tokens within 2^32 bytes
+  const bool small = a.cache.page_shift < 4 || !near(a.cache.ku) || !near(a.cache.vu);
+  if (cache_dtype == SV_E4M3)
+    small ? launch_dims<true, true>(a, p, stream) : launch_dims<true, false>(a, p, stream);
+  else
+    small ? launch_dims<false, true>(a, p, stream) : launch_dims<false, false>(a, p, stream);
   return hipGetLastError();
 }
 

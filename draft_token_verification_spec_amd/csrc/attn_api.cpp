@@ -39,7 +39,7 @@ int check_cache(const sv_paged_cache* c, int B, bool empty) {
   const int64_t unit = c->dtype == SV_BF16 ? 8 : 16;  // elements of 16 bytes
   for (int64_t s : {c->k_page_stride, c->k_token_stride, c->k_head_stride, c->v_page_stride, c->v_token_stride,
                     c->v_head_stride})
-    if (s < 0 || s % unit != 0) return SV_ERR_INVALID_ARG;
+    if (s < 0 || s % unit != 0 || s / unit > int64_t(0xffffffffu)) return SV_ERR_INVALID_ARG;
   for (int64_t s : {c->k_page_stride, c->v_page_stride})
     if (c->num_pages > 1 && s < c->head_dim) return SV_ERR_INVALID_ARG;
   if (!write_strides_ok(c->page_size, c->heads, c->head_dim, c->k_token_stride, c->k_head_stride) ||
@@ -257,7 +257,21 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
   a.kv_len = kv_len;
   a.scale = scale;
   a.window = window;
-  a.cache = view_of(cache);
+  const PagedView v = view_of(cache);
+  const int shift = cache->dtype == SV_BF16 ? 3 : 4;  // elements of 16 bytes
+  a.cache.table = v.table;
+  a.cache.table_stride = v.table_stride;
+  a.cache.k = v.k;
+  a.cache.v = v.v;
+  a.cache.k_scale = v.k_scale;
+  a.cache.v_scale = v.v_scale;
+  a.cache.ku = {uint32_t(v.k_page >> shift), uint32_t(v.k_token >> shift), uint32_t(v.k_head >> shift)};
+  a.cache.vu = {uint32_t(v.v_page >> shift), uint32_t(v.v_token >> shift), uint32_t(v.v_head >> shift)};
+  a.cache.max_pages = v.max_pages;
+  a.cache.num_pages = v.num_pages;
+  a.cache.heads = v.heads;
+  a.cache.D = v.D;
+  a.cache.page_shift = v.page_shift;
   return to_status(launch_attention(a, p, cache->dtype, static_cast<hipStream_t>(stream)));
 }
 

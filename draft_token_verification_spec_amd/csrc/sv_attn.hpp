@@ -51,6 +51,23 @@ struct GatherArgs {
 };
 hipError_t launch_gather(const GatherArgs& a, int out_dtype, int cache_dtype, hipStream_t stream);
 
+// Strides in units of 16 bytes.
+struct UnitStrides {
+  uint32_t page, token, head;
+};
+
+// A cache as the attention reads it.
+struct CacheView {
+  const int32_t* table;
+  int64_t table_stride;
+  const void* k;
+  const void* v;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  UnitStrides ku, vu;
+  int max_pages, num_pages, heads, D, page_shift;
+};
+
 struct AttnArgs {
   int B, T, q_heads;
   RowsIn q;
@@ -60,14 +77,15 @@ struct AttnArgs {
   const int32_t* kv_len;
   float scale;
   int window;  // 0: none
-  PagedView cache;
+  CacheView cache;
 };
 
-// How a call is divided: row_tile rows a workgroup, contexts in splits
+// How a call is divided: row_tile rows a workgroup, `tiles` workgroups for a
+// request's rows, contexts in splits
 // of split_len tokens (the last one takes what is left).  The parts of split s
 // and row t, head h are at (s * T + t) * q_heads + h.
 struct AttnPlan {
-  int row_tile, split_len, num_splits;
+  int row_tile, tiles, split_len, num_splits;
   size_t ml_bytes, o_bytes;
   float2* part_ml;  // maximum (base-2 logarithm), sum of weights
   float* part_o;    // weighted values
