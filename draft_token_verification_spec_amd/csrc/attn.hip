@@ -453,18 +453,26 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, const f
                                                  0);
 }
 
+// Nothing moves across: left alone, the compiler reads a product's operand from
+// LDS right before its use and waits for it.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kManyRows = 32 * kAttnWaves;
 
-template <int DP, bool FP8, bool SMALL>
-__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kernel(AttnArgs a, AttnPlan p) {
+// PAGES: 0 pages of fewer than 16 tokens (or rows too far apart for a 32-bit
+// offset), every thread looks its tokens' pages up; 1 a load's tokens of a wave
+// lie in one page; 2 the tile lies in one page.
+template <int DP, bool FP8, int PAGES>
+__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void many_rows_kernel(AttnArgs a, AttnPlan p) {
   constexpr int M = kManyRows;
   constexpr int kSteps = DP / 16;
   constexpr int kDT = DP / 32;
-  constexpr int kLanes = FP8 ? DP / 16 : DP / 8;      // that load a token's row, 16 bytes each
-  constexpr int kSpan = kAttnThreads / kLanes;        // tokens of one load of the workgroup
+  constexpr int kLanes = FP8 ? DP / 16 : DP / 8;  // that load a token's row, 16 bytes each
+  constexpr int kSpan = kAttnThreads / kLanes;    // tokens of one load of the workgroup
+  constexpr int kWaveSpan = 64 / kLanes;          // and of a wave
   constexpr int kLoads = kTile / kSpan;
-  constexpr int kParts = FP8 ? 2 : 1;                 // 8 channels each, of a load
+  constexpr int kParts = FP8 ? 2 : 1;             // 8 channels each, of a load
   __shared__ __align__(16) uint16_t keys[2][kTile * kPitch<DP>];
   __shared__ __align__(16) uint16_t values[2][kTile * kValuePitch<DP>];
   __shared__ __align__(16) uint8_t state[2][kTile];   // of a token: 0 present, 1 absent, 2 a value not finite
@@ -487,162 +495,199 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
   const int b = at_x / p.tiles;
   // later tiles of a prompt see more: they start first
   for (int64_t first_row = int64_t(p.tiles - 1 - (at_x - b * p.tiles)) * M;; first_row += int64_t(p.tiles) * M) {
-  const Tile t = tile_at<M>(a, G, b, first_row);
-  if (t.rows == 0) return;
-  const Splits live = live_splits(t, p.split_len, p.num_splits);
-  if (split < live.first || split > live.last) continue;
-  const int begin = max(t.begin, split * p.split_len) & ~(kTile - 1);
-  const int end = split == p.num_splits - 1 ? t.end : min(t.end, (split + 1) * p.split_len);
+    const Tile t = tile_at<M>(a, G, b, first_row);
+    if (t.rows == 0) return;
+    const Splits live = live_splits(t, p.split_len, p.num_splits);
+    if (split < live.first || split > live.last) continue;
+    const int begin = max(t.begin, split * p.split_len) & ~(kTile - 1);
+    const int end = split == p.num_splits - 1 ? t.end : min(t.end, (split + 1) * p.split_len);
 
-  const int chunks = c.D >> 3;
-  const int row = 32 * wave + r;
-  const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
-  const int place = row < t.rows ? t.place0 + tok : -1;
-  const int oldest = a.window > 0 ? max(place, -1) - a.window : -1;  // the row sees the tokens oldest < j <= place
-  uint4 qf[kSteps];
-  {
-    const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
+    int place;
+    uint4 qf[kSteps];
+    {
+      const int row = 32 * wave + r;
+      const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
+      place = row < t.rows ? t.place0 + tok : -1;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      qf[s] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < t.rows && 2 * s + h < chunks) qf[s] = *reinterpret_cast<const uint4*>(q + 8 * (2 * s + h));
-    }
-  }
-  const int first_place = t.place0 + t.first_row / G;
-  const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
-  // of this wave's rows
-  const int wave_first = t.place0 + (t.first_row + 32 * wave) / G;
-  const int wave_last = 32 * wave < t.rows ? t.place0 + (t.first_row + min(32 * wave + 31, t.rows - 1)) / G : -1;
-  const float sc = a.scale * kLog2e;
-
-  f32x16 o[kDT];
-#pragma unroll
-  for (int d = 0; d < kDT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  float mx = -INFINITY, l = 0.f;
-
-  // staging: thread -> token kSpan * i + tid / kLanes, 16 bytes tid % kLanes;
-  // a wave's kWaveSpan tokens of a load lie in one page unless SMALL
-  constexpr int kWaveSpan = 64 / kLanes;
-  uint4 kr[kLoads], vr[kLoads];
-  uint32_t ks[kLoads], vs[kLoads];
-  int page[kLoads];
-  const int64_t table = b * c.table_stride;
-  const int in_page = (1 << c.page_shift) - 1;
-  const int own = SMALL ? tid / kLanes : wave * kWaveSpan;  // of a load's tokens, the first that `page` is of
-  const int from = SMALL ? 0 : lane / kLanes;               // this thread's token behind it
-  auto pages = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int j = min(base + kSpan * i + own, end - 1);
-      page[i] = SMALL ? c.table[table + (j >> c.page_shift)] : uniform_at(c.table, table + (j >> c.page_shift));
-    }
-  };
-  uint32_t lane_at[2];  // bytes from that token's row
-  {
-    const uint32_t unit = min(tid % kLanes, (FP8 ? c.D >> 4 : chunks) - 1);
-    lane_at[0] = (uint32_t(from) * c.ku.token + unit) << 4;
-    lane_at[1] = (uint32_t(from) * c.vu.token + unit) << 4;
-  }
-  uint32_t absent;  // bit i: load i's token is absent
-  auto request = [&](int base) {
-    absent = 0;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int j = base + kSpan * i + own;
-      const bool found = uint32_t(page[i]) < uint32_t(c.num_pages);
-      absent |= uint32_t(!found || j + from >= end) << i;
-      const int at = found ? page[i] : 0, slot = j & in_page;
-      kr[i] = load_from(static_cast<const char*>(c.k) + row_at(c.ku, at, slot, kvh), lane_at[0]);
-      vr[i] = load_from(static_cast<const char*>(c.v) + row_at(c.vu, at, slot, kvh), lane_at[1]);
-      if (FP8) {
-        const int64_t so = ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot;
-        ks[i] = c.k_scale[so + from];
-        vs[i] = c.v_scale[so + from];
+      for (int s = 0; s < kSteps; ++s) {
+        qf[s] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < t.rows && 8 * (2 * s + h) < c.D) qf[s] = *reinterpret_cast<const uint4*>(q + 8 * (2 * s + h));
       }
     }
-  };
-  // every row of the tile sees all 64 tokens, as far as places go
-  auto whole = [&](int base) {
-    return base + kTile - 1 <= first_place && base + kTile <= end && (a.window == 0 || base > last_place - a.window);
-  };
-  auto stage = [&](int base, int buf) {
-    const bool ok = whole(base);
+    const int oldest = a.window > 0 ? max(place, -1) - a.window : -1;  // the row sees the tokens oldest < j <= place
+    const int first_place = t.place0 + t.first_row / G;
+    const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
+    const float sc = a.scale * kLog2e;
+
+    f32x16 o[kDT];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int at = kSpan * i + tid / kLanes;
-      uint4 kw[kParts], vw[kParts];
-      if (FP8) {
-        kw[0] = dequant8(make_uint2(kr[i].x, kr[i].y), scale_of(ks[i]));
-        kw[kParts - 1] = dequant8(make_uint2(kr[i].z, kr[i].w), scale_of(ks[i]));
-        vw[0] = dequant8(make_uint2(vr[i].x, vr[i].y), scale_of(vs[i]));
-        vw[kParts - 1] = dequant8(make_uint2(vr[i].z, vr[i].w), scale_of(vs[i]));
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    float mx = -INFINITY, l = 0.f;
+
+    // staging: thread -> token kSpan * i + tid / kLanes, 16 bytes tid % kLanes
+    uint4 kin[kLoads], vin[kLoads];
+    uint32_t kscale[kLoads], vscale[kLoads];
+    int page[PAGES == 2 ? 1 : kLoads];  // page table entries: of the tile, of the wave's loads, of the thread's tokens
+    const int64_t table = b * c.table_stride;
+    const int in_page = (1 << c.page_shift) - 1;
+    const int own = PAGES == 0 ? tid / kLanes : wave * kWaveSpan;  // of a load's tokens, the first that `page` is of
+    const int from = PAGES == 0 ? 0 : lane / kLanes;               // this thread's token behind it
+    const uint32_t unit = min(tid % kLanes, (FP8 ? c.D >> 4 : c.D >> 3) - 1);
+    auto pages = [&](int base) {
+      if constexpr (PAGES == 2) {
+        page[0] = uniform_at(c.table, table + (min(base, end - 1) >> c.page_shift));
       } else {
-        kw[0] = kr[i];
-        vw[0] = vr[i];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int j = min(base + kSpan * i + own, end - 1) >> c.page_shift;
+          page[i] = PAGES == 0 ? c.table[table + j] : uniform_at(c.table, table + j);
+        }
       }
-      const bool gone = (absent >> i) & 1u;
-      bool bad = false;
-      if (!ok) {
+    };
+    auto found = [&](int i) { return uint32_t(page[PAGES == 2 ? 0 : i]) < uint32_t(c.num_pages); };
+    auto request = [&](int base, const void* p0, const UnitStrides& u, const uint8_t* scale, uint4 (&in)[kLoads],
+                       uint32_t (&in_scale)[kLoads]) {
+      const uint32_t lane_at = (uint32_t(from) * u.token + unit) << 4;  // bytes from the row of `own`
+      if constexpr (PAGES == 2) {
+        const int at = found(0) ? page[0] : 0, slot = (base + own) & in_page;
+        const char* q = static_cast<const char*>(p0) + row_at(u, at, slot, kvh);
+        const uint8_t* so = FP8 ? scale + ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot : scale;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          in[i] = load_from(q, lane_at);
+          q += uint64_t(u.token) * kSpan << 4;
+          if (FP8) in_scale[i] = so[kSpan * i + from];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = found(i) ? page[i] : 0, slot = (base + kSpan * i + own) & in_page;
+          in[i] = load_from(static_cast<const char*>(p0) + row_at(u, at, slot, kvh), lane_at);
+          if (FP8) in_scale[i] = scale[((int64_t(at) * c.heads + kvh) << c.page_shift) + slot + from];
+        }
+      }
+    };
+    // every row of the tile sees all 64 tokens, as far as places go
+    auto whole = [&](int base) {
+      return base + kTile - 1 <= first_place && base + kTile <= end && (a.window == 0 || base > last_place - a.window);
+    };
+    auto stage_keys = [&](int buf) {
+      uint16_t* const to = &keys[buf][tid / kLanes * kPitch<DP> + 8 * kParts * (tid % kLanes)];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (FP8) {
+          const float scale = scale_of(kscale[i]);
+          *reinterpret_cast<uint4*>(to + kSpan * i * kPitch<DP>) = dequant8(make_uint2(kin[i].x, kin[i].y), scale);
+          *reinterpret_cast<uint4*>(to + kSpan * i * kPitch<DP> + 8) = dequant8(make_uint2(kin[i].z, kin[i].w), scale);
+        } else {
+          *reinterpret_cast<uint4*>(to + kSpan * i * kPitch<DP>) = kin[i];
+        }
+      }
+    };
+    int marked = 0;  // bit buf: this wave has left marks in state[buf] and lacks[buf]
+    auto stage_values = [&](int base, int buf) {
+      const bool ok = whole(base);
+      uint16_t* const to = &values[buf][tid / kLanes * kValuePitch<DP> + 8 * kParts * (tid % kLanes)];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (FP8) {
+          const float scale = scale_of(vscale[i]);
+          *reinterpret_cast<uint4*>(to + kSpan * i * kValuePitch<DP>) = dequant8(make_uint2(vin[i].x, vin[i].y), scale);
+          *reinterpret_cast<uint4*>(to + kSpan * i * kValuePitch<DP> + 8) =
+              dequant8(make_uint2(vin[i].z, vin[i].w), scale);
+        } else {
+          *reinterpret_cast<uint4*>(to + kSpan * i * kValuePitch<DP>) = vin[i];
+        }
+      }
+      bool lack = false;
+#pragma unroll
+      for (int i = 0; i < (PAGES == 2 ? 1 : kLoads); ++i) lack |= !found(i);
+      const bool trouble = !ok || (PAGES == 0 ? __any(lack) : lack);
+      if (!trouble && !((marked >> buf) & 1)) return;
+      // (from here on what was stored is read back: values kept for this in
+      // registers would cost the usual path)
+      asm volatile("" ::: "memory");
+      bool some = false;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = kSpan * i + tid / kLanes;
+        const bool gone = !found(i) || base + at >= end;
         // a weight of zero does not stop a value that is not finite: such
         // values are taken out, and their tokens' scores made NaN instead
+        uint32_t bad = 0;
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) bad |= not_finite8(vw[q]) != 0;
-        const uint64_t any = __ballot(bad && !gone);
-        bad = (any >> (lane & ~(kLanes - 1))) & ((uint64_t(1) << kLanes) - 1);
-      }
-      if (gone || bad) {
+        for (int q = 0; q < kParts; ++q)
+          bad |= not_finite8(*reinterpret_cast<const uint4*>(to + kSpan * i * kValuePitch<DP> + 8 * q));
+        const uint64_t any = __ballot(bad != 0 && !gone);
+        const bool spoiled = (any >> (lane & ~(kLanes - 1))) & ((uint64_t(1) << kLanes) - 1);
+        if (gone || spoiled) {
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) vw[q] = make_uint4(0u, 0u, 0u, 0u);
+          for (int q = 0; q < kParts; ++q)
+            *reinterpret_cast<uint4*>(to + kSpan * i * kValuePitch<DP> + 8 * q) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (tid % kLanes == 0) state[buf][at] = gone ? 1 : spoiled ? 2 : 0;
+        some |= gone;
       }
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        const int e = 8 * (kParts * (tid % kLanes) + q);
-        *reinterpret_cast<uint4*>(&keys[buf][at * kPitch<DP> + e]) = kw[q];
-        *reinterpret_cast<uint4*>(&values[buf][at * kValuePitch<DP> + e]) = vw[q];
-      }
-      if (tid % kLanes == 0) state[buf][at] = gone ? 1 : bad ? 2 : 0;
-    }
-    const bool some = __any(absent != 0);
-    if (lane == 0) lacks[buf][wave] = some;
-  };
+      some = __any(some);
+      if (lane == 0) lacks[buf][wave] = some;
+      marked = trouble ? marked | (1 << buf) : marked & ~(1 << buf);
+    };
 
-  int buf = 0;
-  if (begin < end) {
-    pages(begin);
-    request(begin);
-    pages(begin + kTile);
-    stage(begin, 0);
-  }
-  __syncthreads();
-  for (int base = begin; base < end; base += kTile) {
-    const bool more = base + kTile < end;
-    if (more) request(base + kTile);
-    // a wave whose rows see nothing here only helps to load
-    const bool sees_some = base <= wave_last && (a.window == 0 || base + kTile - 1 > wave_first - a.window);
-    f32x16 s[2];
-    if (sees_some) {
-      const uint16_t* const kt = &keys[buf][r * kPitch<DP> + 8 * h];
+    // (the barrier that ended the loop has ended every read of a former tile)
+    if (tid < kTile) state[0][tid] = state[1][tid] = 0;
+    if (tid < kAttnWaves) lacks[0][tid] = lacks[1][tid] = 0;
+    __syncthreads();
+    int buf = 0;
+    if (begin < end) {
+      pages(begin);
+      request(begin, c.k, c.ku, c.k_scale, kin, kscale);
+      request(begin, c.v, c.vu, c.v_scale, vin, vscale);
+      stage_keys(0);
+      stage_values(begin, 0);
+      pages(begin + kTile);
+    }
+    __syncthreads();
+    // One tile: its successor is asked for first and staged last (behind the
+    // last tile the same slots of the last page, which nothing reads), without
+    // a branch on the way that would hold the loads up.
+    for (int base = begin; base < end; base += kTile) {
+      const int next = base + kTile;
+      request(next, c.k, c.ku, c.k_scale, kin, kscale);
+      request(next, c.v, c.vu, c.v_scale, vin, vscale);
+      f32x16 s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+      // products in groups of four, whose operands are read a group ahead; a wave
+      // that has products to issue goes before one in its softmax (349 -> 343 us)
+      {
+        const uint16_t* const kt = &keys[buf][r * kPitch<DP> + 8 * h];
+        uint4 kf[2][4];
+        auto read = [&](int n) {
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st)
+          for (int i = 0; i < 4; ++i)
+            kf[(n >> 2) & 1][i] =
+                *reinterpret_cast<const uint4*>(kt + 32 * ((n + i) & 1) * kPitch<DP> + 16 * ((n + i) >> 1));
+        };
+        read(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4 kf = *reinterpret_cast<const uint4*>(kt + 32 * u * kPitch<DP> + 16 * st);
-          s[u] = mfma32(kf, qf[st], s[u]);
+        for (int n = 0; n < 2 * kSteps; n += 4) {
+          if (n + 4 < 2 * kSteps) read(n + 4);
+          keep_order();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[(n + i) & 1] = mfma32(kf[(n >> 2) & 1][i], qf[(n + i) >> 1], s[(n + i) & 1]);
+          keep_order();
         }
-    }
-    // (here, ahead of the softmax: a scalar load in flight holds up LDS reads)
-    if (more) pages(base + 2 * kTile);
-    if (sees_some) {
+      }
+      __builtin_amdgcn_s_setprio(0);
       const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
-      const bool masked = !whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0;
-      const uint16_t* const vt = &values[buf][(4 * h + ((lane & 15) >> 2)) * kValuePitch<DP> + (lane & 16) + 4 * (lane & 3)];
-      if (masked) {
+      if (!whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -665,72 +710,95 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : 2) void many_rows_kern
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       if (__any(top > mx)) {
-        const float next = fmaxf(mx, top);
-        const float keep = fast_exp2((mx - (next == -INFINITY ? 0.f : next)) * sc);
-        mx = next;
+        const float higher = fmaxf(mx, top);
+        const float keep = fast_exp2((mx - (higher == -INFINITY ? 0.f : higher)) * sc);
+        mx = higher;
         l *= keep;
 #pragma unroll
         for (int d = 0; d < kDT; ++d) o[d] *= keep;
       }
       const float ref = mx == -INFINITY ? 0.f : mx * sc;
+      const uint16_t* const vt =
+          &values[buf][(4 * h + ((lane & 15) >> 2)) * kValuePitch<DP> + (lane & 16) + 4 * (lane & 3)];
+      uint4 vf[2][4];
+      auto read_values = [&](int n) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int i = 0; i < 4; ++i) {
+          const int at = n + i, d = at % kDT, t16 = at / kDT;  // channels 32 d .., tokens 16 t16 ..
+          const uint2 v0 = read_transposed(vt + 16 * t16 * kValuePitch<DP> + 32 * d);
+          const uint2 v1 = read_transposed(vt + (16 * t16 + 8) * kValuePitch<DP> + 32 * d);
+          vf[(n >> 2) & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        }
+      };
+      read_values(0);
+      uint4 pf[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           s[u][i] = fast_exp2(fmaf(s[u][i], sc, -ref));
           l += s[u][i];
         }
+        // rounded to bf16 for the product: a weight of at most 1 is off by 2^-8 of itself
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int q = 0; q < 2; ++q)
+          pf[u][q] = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
+                                pack_bf16(s[u][8 * q + 4], s[u][8 * q + 5]),
+                                pack_bf16(s[u][8 * q + 6], s[u][8 * q + 7]));
+      }
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          // rounded to bf16 for the product: a weight of at most 1 is off by 2^-8 of itself
-          const uint4 pf = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
-                                      pack_bf16(s[u][8 * q + 4], s[u][8 * q + 5]),
-                                      pack_bf16(s[u][8 * q + 6], s[u][8 * q + 7]));
+      for (int n = 0; n < 4 * kDT; n += 4) {
+        if (n + 4 < 4 * kDT) read_values(n + 4);
+        keep_order();
 #pragma unroll
-          for (int d = 0; d < kDT; ++d) {
-            const uint2 v0 = read_transposed(vt + (32 * u + 16 * q) * kValuePitch<DP> + 32 * d);
-            const uint2 v1 = read_transposed(vt + (32 * u + 16 * q + 8) * kValuePitch<DP> + 32 * d);
-            o[d] = mfma32(make_uint4(v0.x, v0.y, v1.x, v1.y), pf, o[d]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int at = n + i, d = at % kDT, t16 = at / kDT;
+          o[d] = mfma32(vf[(n >> 2) & 1][i], pf[t16 >> 1][t16 & 1], o[d]);
         }
+        keep_order();
+      }
+      __builtin_amdgcn_s_setprio(0);
+      stage_keys(buf ^ 1);
+      stage_values(next, buf ^ 1);
+      pages(next + kTile);
+      buf ^= 1;
+      __syncthreads();
     }
-    if (more) stage(base + kTile, buf ^ 1);
-    buf ^= 1;
-    __syncthreads();
-  }
 
-  l += __shfl_xor(l, 32, 64);
-  if (row >= t.rows) continue;  // (the barriers above have ended every wave's reads of LDS)
-  const float ref = mx == -INFINITY ? 0.f : mx * sc;
-  const int64_t at = int64_t(t.token0 + tok) * a.q_heads + head;
-  if (live.first == live.last) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* out = static_cast<uint16_t*>(a.out.p) + int64_t(t.token0 + tok) * a.out.token + head * a.out.head;
+    l += __shfl_xor(l, 32, 64);
+    int row = 32 * wave + r;
+    asm volatile("" : "+v"(row));  // (what follows from it is formed here, not kept in registers through the loop)
+    if (row >= t.rows) continue;
+    const int tok = t.token0 + (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
+    const float ref = mx == -INFINITY ? 0.f : mx * sc;
+    const int64_t at = int64_t(tok) * a.q_heads + head;
+    if (live.first == live.last) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* out = static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head;
 #pragma unroll
-    for (int d = 0; d < kDT; ++d)
+      for (int d = 0; d < kDT; ++d)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = 32 * d + 8 * k + 4 * h;
-        if (e < c.D)
-          *reinterpret_cast<uint2*>(out + e) = make_uint2(pack_bf16(o[d][4 * k] * inv, o[d][4 * k + 1] * inv),
-                                                          pack_bf16(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv));
-      }
-    if (a.lse && h == 0) a.lse[at] = l == 0.f ? -INFINITY : (ref + fast_log2(l)) * kLn2;
-  } else {
-    const int64_t part = split * (int64_t(a.T) * a.q_heads) + at;
+        for (int k = 0; k < 4; ++k) {
+          const int e = 32 * d + 8 * k + 4 * h;
+          if (e < c.D)
+            *reinterpret_cast<uint2*>(out + e) = make_uint2(pack_bf16(o[d][4 * k] * inv, o[d][4 * k + 1] * inv),
+                                                            pack_bf16(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv));
+        }
+      if (a.lse && h == 0) a.lse[at] = l == 0.f ? -INFINITY : (ref + fast_log2(l)) * kLn2;
+    } else {
+      const int64_t part = split * (int64_t(a.T) * a.q_heads) + at;
 #pragma unroll
-    for (int d = 0; d < kDT; ++d)
+      for (int d = 0; d < kDT; ++d)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = 32 * d + 8 * k + 4 * h;
-        if (e < c.D)
-          *reinterpret_cast<float4*>(p.part_o + part * c.D + e) =
-              make_float4(o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]);
-      }
-    if (h == 0) p.part_ml[part] = make_float2(mx == -INFINITY ? mx : ref, l);
-  }
+        for (int k = 0; k < 4; ++k) {
+          const int e = 32 * d + 8 * k + 4 * h;
+          if (e < c.D)
+            *reinterpret_cast<float4*>(p.part_o + part * c.D + e) =
+                make_float4(o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]);
+        }
+      if (h == 0) p.part_ml[part] = make_float2(mx == -INFINITY ? mx : ref, l);
+    }
   }
 }
 
@@ -800,7 +868,12 @@ void launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   } else if (p.row_tile == 32) {
     launch_few<DP, 2, FP8, SMALL>(a, p, grid, stream);
   } else if (p.row_tile == kManyRows) {
-    hipLaunchKernelGGL((many_rows_kernel<DP, FP8, SMALL>), grid, dim3(kAttnThreads), 0, stream, a, p);
+    if (SMALL)
+      hipLaunchKernelGGL((many_rows_kernel<DP, FP8, 0>), grid, dim3(kAttnThreads), 0, stream, a, p);
+    else if (a.cache.page_shift < 6)
+      hipLaunchKernelGGL((many_rows_kernel<DP, FP8, 1>), grid, dim3(kAttnThreads), 0, stream, a, p);
+    else
+      hipLaunchKernelGGL((many_rows_kernel<DP, FP8, 2>), grid, dim3(kAttnThreads), 0, stream, a, p);
     launch_join<kManyRows>(a, p, stream);
   } else if constexpr (DP < 256) {
     launch_few<DP, 4, FP8, SMALL>(a, p, grid, stream);
