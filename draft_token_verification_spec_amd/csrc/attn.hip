@@ -109,6 +109,20 @@ __device__ __forceinline__ uint32_t not_finite8(const uint4& w) {
   return (not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w)) & 0x80008000u;
 }
 
+// The larger of a value and that of the lane 32 away, or 16 and 32 away.
+__device__ __forceinline__ float max_over_halves(float x) {
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+__device__ __forceinline__ float max_over_quarters(float x) {
+  const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max_over_halves(fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])));
+}
+
+// Nothing moves across: left alone, the compiler reads a product's operand from
+// LDS right before its use and waits for it.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 __device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
@@ -204,7 +218,8 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
   const int in_page = (1 << c.page_shift) - 1;
   // the page table's entries of the block's tokens 0 .. 15 and 16 .. 31 (SMALL:
   // of this lane's, r and 16 + r), or of the last token in their place
-  auto pages = [&](int base, int (&page)[2]) {
+  int page[2];
+  auto pages = [&](int base) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = min(base + 16 * h + (SMALL ? r : 0), end - 1);
@@ -220,58 +235,58 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
     lane_at[0][i] = (uint32_t(SMALL ? 0 : r) * c.ku.token + unit) << 4;
     lane_at[1][i] = (uint32_t(SMALL ? 0 : r) * c.vu.token + unit) << 4;
   }
-  auto request = [&](int base, const int (&page)[2]) {
+  auto request = [&](int base, const void* p0, const UnitStrides& u, const uint32_t (&at_lane)[kLoads],
+                     const uint8_t* scale, uint4 (&in)[2][kLoads], uint32_t (&in_scale)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int j = base + 16 * h + (SMALL ? r : 0);
-      const bool found = uint32_t(page[h]) < uint32_t(c.num_pages);
-      const int at = found ? page[h] : 0, slot = j & in_page;
-      have[h] = found && j + (SMALL ? 0 : r) < end;
-      const char* kp = static_cast<const char*>(c.k) + row_at(c.ku, at, slot, kvh);
-      const char* vp = static_cast<const char*>(c.v) + row_at(c.vu, at, slot, kvh);
+      const int at = uint32_t(page[h]) < uint32_t(c.num_pages) ? page[h] : 0;
+      const int slot = (base + 16 * h + (SMALL ? r : 0)) & in_page;
+      const char* q = static_cast<const char*>(p0) + row_at(u, at, slot, kvh);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        kr[h][i] = load_from(kp, lane_at[0][i]);
-        vr[h][i] = load_from(vp, lane_at[1][i]);
-      }
-      if (FP8) {
-        const int64_t so = ((int64_t(at) * c.heads + kvh) << c.page_shift) + slot;
-        ks[h] = c.k_scale[so + (SMALL ? 0 : r)];
-        vs[h] = c.v_scale[so + (SMALL ? 0 : r)];
-      }
+      for (int i = 0; i < kLoads; ++i) in[h][i] = load_from(q, at_lane[i]);
+      if (FP8) in_scale[h] = scale[((int64_t(at) * c.heads + kvh) << c.page_shift) + slot + (SMALL ? 0 : r)];
     }
+  };
+  auto request_keys = [&](int base) { request(base, c.k, c.ku, lane_at[0], c.k_scale, kr, ks); };
+  auto request_values = [&](int base) {
+    request(base, c.v, c.vu, lane_at[1], c.v_scale, vr, vs);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      have[h] = uint32_t(page[h]) < uint32_t(c.num_pages) && base + 16 * h + r < end;
   };
 
   const int stride = kAttnWaves * kBlock;
   int base = begin + wave * kBlock;
-  int page[2];
   if (base < end) {
-    pages(base, page);
-    request(base, page);
-    pages(base + stride, page);
+    pages(base);
+    request_keys(base);
+    request_values(base);
+    pages(base + stride);
   }
   uint16_t* const mine = values[wave];
   for (; base < end; base += stride) {
     // S^T, a block's 16 tokens by 16 rows at a time
     f32x4 s[2][MT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int m = 0; m < MT; ++m) s[h][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const float kscale = FP8 ? scale_of(ks[h]) : 1.f;
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint4 kf;
         if (FP8) {
           const uint4 w = kr[h][st >> 1];
-          kf = dequant8((st & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), kscale);
+          kf = dequant8((st & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), scale_of(ks[h]));
         } else {
           kf = kr[h][st];
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[h][m] = mfma16(kf, qf[m][st], s[h][m]);
       }
-    }
+    const bool more = base + stride < end;
+    if (more) request_keys(base + stride);
     // every row sees every token of the block, unless it reaches beyond the
     // first row's place or the last row's window, or lacks tokens
     const bool whole = __all(have[0] && have[1]) && base + kBlock - 1 <= first_place &&
@@ -313,17 +328,16 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
         }
       }
     }
-    const int now = base;
-    if (base + stride < end) {
-      request(base + stride, page);
-      pages(base + 2 * stride, page);
+    if (more) {
+      request_values(base + stride);
+      pages(base + 2 * stride);
     }
     if (!whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int k = 16 * h + 4 * g + i, j = now + k;
+          const int k = 16 * h + 4 * g + i, j = base + k;
           const bool off = (hidden >> k) & 1u, bad = (nan >> k) & 1u;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -333,6 +347,18 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
           }
         }
     }
+    // values are read from LDS four channel tiles ahead of their products
+    uint4 vf[2][4];
+    const uint16_t* const vt = mine + (4 * g + (r >> 2)) * kPitch<DP> + 4 * (r & 3);
+    auto read_values = [&](int d) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 v0 = read_transposed(vt + 16 * (d + i));
+        const uint2 v1 = read_transposed(vt + 16 * kPitch<DP> + 16 * (d + i));
+        vf[(d >> 2) & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      }
+    };
+    read_values(0);
     // weights, in place of the scores, and the running statistics
     uint4 pf[MT];
 #pragma unroll
@@ -342,8 +368,7 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[h][m][i]);
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      top = max_over_quarters(top);
       const float next = fmaxf(mx[m], top);
       const float ref = next == -INFINITY ? 0.f : next * sc;
       const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
@@ -363,14 +388,15 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
 #pragma unroll
       for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
     }
-    const uint16_t* const vt = mine + (4 * g + (r >> 2)) * kPitch<DP> + 4 * (r & 3);
 #pragma unroll
-    for (int d = 0; d < kDT; ++d) {
-      const uint2 v0 = read_transposed(vt + 16 * d);
-      const uint2 v1 = read_transposed(vt + 16 * kPitch<DP> + 16 * d);
-      const uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
+    for (int d = 0; d < kDT; d += 4) {
+      if (d + 4 < kDT) read_values(d + 4);
+      keep_order();
 #pragma unroll
-      for (int m = 0; m < MT; ++m) o[d][m] = mfma16(vf, pf[m], o[d][m]);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) o[d + i][m] = mfma16(vf[(d >> 2) & 1][i], pf[m], o[d + i][m]);
+      keep_order();
     }
   }
 
@@ -452,10 +478,6 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, const f
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
 }
-
-// Nothing moves across: left alone, the compiler reads a product's operand from
-// LDS right before its use and waits for it.
-__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kManyRows = 32 * kAttnWaves;
@@ -708,7 +730,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      top = max_over_halves(top);
       if (__any(top > mx)) {
         const float higher = fmaxf(mx, top);
         const float keep = fast_exp2((mx - (higher == -INFINITY ? 0.f : higher)) * sc);
