@@ -53,6 +53,17 @@ __device__ __forceinline__ uint4 load_from(const char* p, uint32_t at) {
   return *reinterpret_cast<const uint4*>(p + at);
 }
 
+// Workgroups go to the 8 XCDs in turn, so with an even grid one XCD would get
+// the same request for every head and split, and requests of different lengths
+// load the XCDs unevenly: blocks of 8 positions are turned by one from head to
+// head and from split to split (a decoding batch of 64 at 1024 to 4096 tokens:
+// 155 -> 142 us).
+__device__ __forceinline__ uint32_t spread_over_xcds(uint32_t x, uint32_t head, uint32_t split) {
+  if ((x | 7u) >= gridDim.x) return x;
+  const uint32_t turn = ((gridDim.x & 1u) ? 0u : head) + ((gridDim.x & gridDim.y & 1u) ? 0u : split);
+  return (x & ~7u) | ((x + turn) & 7u);
+}
+
 // One tile of rows of one request.
 struct Tile {
   int first_row;   // tile's first row in the request (row = token * G + head in group)
@@ -170,8 +181,9 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
   const int r = lane & 15, g = lane >> 4;
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int G = a.q_heads / c.heads;
-  const int b = blockIdx.x / p.tiles;
-  for (int64_t first_row = int64_t(blockIdx.x - b * p.tiles) * M;; first_row += int64_t(p.tiles) * M) {
+  const int at_x = spread_over_xcds(blockIdx.x, kvh, split);
+  const int b = at_x / p.tiles;
+  for (int64_t first_row = int64_t(at_x - b * p.tiles) * M;; first_row += int64_t(p.tiles) * M) {
   const Tile t = tile_at<M>(a, G, b, first_row);
   if (t.rows == 0) return;
   const Splits live = live_splits(t, p.split_len, p.num_splits);
@@ -235,6 +247,7 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
     lane_at[0][i] = (uint32_t(SMALL ? 0 : r) * c.ku.token + unit) << 4;
     lane_at[1][i] = (uint32_t(SMALL ? 0 : r) * c.vu.token + unit) << 4;
   }
+  uint32_t lanes = ~0u;
   auto request = [&](int base, const void* p0, const UnitStrides& u, const uint32_t (&at_lane)[kLoads],
                      const uint8_t* scale, uint4 (&in)[2][kLoads], uint32_t (&in_scale)[2]) {
 #pragma unroll
@@ -243,7 +256,7 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
       const int slot = (base + 16 * h + (SMALL ? r : 0)) & in_page;
       const char* q = static_cast<const char*>(p0) + row_at(u, at, slot, kvh);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) in[h][i] = load_from(q, at_lane[i]);
+      for (int i = 0; i < kLoads; ++i) in[h][i] = load_from(q, at_lane[i] & lanes);
       if (FP8) in_scale[h] = scale[((int64_t(at) * c.heads + kvh) << c.page_shift) + slot + (SMALL ? 0 : r)];
     }
   };
@@ -257,14 +270,13 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
 
   const int stride = kAttnWaves * kBlock;
   int base = begin + wave * kBlock;
-  if (base < end) {
-    pages(base);
-    request_keys(base);
-    request_values(base);
-    pages(base + stride);
-  }
   uint16_t* const mine = values[wave];
-  for (; base < end; base += stride) {
+  if (base < end) {
+  pages(base);
+  request_keys(base);
+  request_values(base);
+  pages(base + stride < end ? base + stride : base);
+  do {
     // S^T, a block's 16 tokens by 16 rows at a time
     f32x4 s[2][MT];
 #pragma unroll
@@ -285,8 +297,13 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[h][m] = mfma16(kf, qf[m][st], s[h][m]);
       }
+    // Behind the wave's last block every lane asks for one word of the same
+    // block again, which nothing reads: loads on one path only would have to be
+    // waited for as if on the other.
     const bool more = base + stride < end;
-    if (more) request_keys(base + stride);
+    const int next = more ? base + stride : base;
+    lanes = more ? ~0u : 0u;
+    request_keys(next);
     // every row sees every token of the block, unless it reaches beyond the
     // first row's place or the last row's window, or lacks tokens
     const bool whole = __all(have[0] && have[1]) && base + kBlock - 1 <= first_place &&
@@ -328,10 +345,8 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
         }
       }
     }
-    if (more) {
-      request_values(base + stride);
-      pages(base + 2 * stride);
-    }
+    request_values(next);
+    pages(next + stride < end ? next + stride : next);
     if (!whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -398,6 +413,8 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
         for (int m = 0; m < MT; ++m) o[d + i][m] = mfma16(vf[(d >> 2) & 1][i], pf[m], o[d + i][m]);
       keep_order();
     }
+    base += stride;
+  } while (base < end);
   }
 
   // join the waves: the tile's maximum, then each wave's results scaled to it
@@ -513,6 +530,8 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
     const uint32_t pos = (i & 7) * per + (i >> 3);
     kvh = pos / gridDim.x;
     at_x = pos - kvh * gridDim.x;
+  } else {
+    at_x = spread_over_xcds(blockIdx.x, kvh, split);
   }
   const int b = at_x / p.tiles;
   // later tiles of a prompt see more: they start first
@@ -828,51 +847,65 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
 // joining splits
 // ---------------------------------------------------------------------------
 
-// One wave per row and head: the splits' maxima and sums give each split's
-// weight, then the weighted values are summed, four channels a lane.
+// One workgroup per row and head.  Every wave forms the row's maximum and sum
+// from the splits' (a lane each); then groups of 32 (64 above 128 channels)
+// lanes take the splits in turn, four channels a lane, and are added in LDS.
 template <int M>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan p) {
+  __shared__ float4 part[kAttnThreads];
   const CacheView& c = a.cache;
-  const int lane = threadIdx.x & 63;
-  const int64_t at = int64_t(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6);
-  const int64_t all = int64_t(a.T) * a.q_heads;
-  if (at >= all) return;
-  const int tok = int(at / a.q_heads), head = int(at % a.q_heads);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int tok = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
+  const int64_t at = blockIdx.x, all = int64_t(a.T) * a.q_heads;
   const int G = a.q_heads / c.heads;
-  const int b = find_sequence(a.query_start, a.B, tok, lane);
-  if (b < 0 || tok >= a.query_start[b + 1]) return;
+  const int b = uniform(find_sequence(a.query_start, a.B, tok, lane));
+  if (b < 0 || tok >= uniform_at(a.query_start, b + 1)) return;
   // the row's tile, as the kernel that wrote the parts saw it
-  const int64_t row = int64_t(tok - a.query_start[b]) * G + head % G;
-  const Tile t = tile_at<M>(a, G, uniform(b), uniform(int(row / M)) * int64_t(M));
+  const int64_t row = int64_t(tok - uniform_at(a.query_start, b)) * G + head % G;
+  const Tile t = tile_at<M>(a, G, b, uniform(int(row / M)) * int64_t(M));
   if (t.rows == 0) return;
   const Splits live = live_splits(t, p.split_len, p.num_splits);
   if (live.first == live.last) return;  // written by the split itself
   float top = -INFINITY;
-  for (int s = live.first; s <= live.last; ++s) top = fmaxf(top, p.part_ml[s * all + at].x);
+  for (int s = live.first + lane; s <= live.last; s += 64) top = fmaxf(top, p.part_ml[s * all + at].x);
+#pragma unroll
+  for (int i = 32; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
   const float ref = top == -INFINITY ? 0.f : top;
-  float total = 0.f, y[4] = {};
-  const bool mine = 4 * lane < c.D;
-  for (int s = live.first; s <= live.last; ++s) {
+  float total = 0.f;
+  for (int s = live.first + lane; s <= live.last; s += 64) {
     const float2 ml = p.part_ml[s * all + at];
-    const float w = fast_exp2(ml.x - ref);
-    total = fmaf(w, ml.y, total);
-    if (mine) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + 4 * lane);
-      y[0] = fmaf(w, v.x, y[0]), y[1] = fmaf(w, v.y, y[1]), y[2] = fmaf(w, v.z, y[2]), y[3] = fmaf(w, v.w, y[3]);
+    total = fmaf(fast_exp2(ml.x - ref), ml.y, total);
+  }
+  total = wave_sum(total);
+  const int lg = c.D <= 128 ? 5 : 6, groups = kAttnThreads >> lg;
+  const int ch = 4 * (tid & ((1 << lg) - 1));
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (ch < c.D) {
+#pragma unroll 4
+    for (int s = live.first + (tid >> lg); s <= live.last; s += groups) {
+      const float w = fast_exp2(p.part_ml[s * all + at].x - ref);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + ch);
+      y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
     }
   }
+  part[tid] = y;
+  __syncthreads();
+  if (tid >> lg) return;
+  for (int i = 1; i < groups; ++i) {
+    const float4 v = part[tid + (i << lg)];
+    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+  }
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  if (mine)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head +
-                              4 * lane) =
-        make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
-  if (a.lse && lane == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
+  if (ch < c.D)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + ch) =
+        make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+  if (a.lse && tid == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
 }
 
 template <int M>
 void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.num_splits == 1) return;
-  const dim3 grid((int64_t(a.T) * a.q_heads + kAttnWaves - 1) / kAttnWaves), block(kAttnThreads);
+  const dim3 grid(a.T * a.q_heads), block(kAttnThreads);
   hipLaunchKernelGGL(join_kernel<M>, grid, block, 0, stream, a, p);
 }
 
@@ -926,11 +959,14 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   const int64_t most_tiles = (1 << 20) / (B > 0 ? B : 1);  // (tiles of all requests and heads: 32 bits)
   tiles = tiles < most_tiles ? tiles : most_tiles;
   p.tiles = int(tiles < 1 ? 1 : tiles);
-  // enough workgroups for every compute unit several times over, of at least
-  // 256 tokens each
+  // enough workgroups to fill the compute units twice over, of at least 256
+  // tokens each; eight times with one tile of rows, whose parts cost little, so
+  // that requests of different lengths even out (1024 to 4096 tokens in a batch
+  // of 64: 151 us filled twice, 142 us eight times; with 5 rows a head of 4096
+  // 8-bit tokens each, 119 and 143 us)
   const int64_t groups = int64_t(B) * p.tiles * kv_heads;
   const int64_t most = (int64_t(max_kv_len) + 255) / 256;
-  const int64_t want = p.row_tile == kManyRows ? 512 : 2048;
+  const int64_t want = p.row_tile == 16 ? 2048 : 512;
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
   n = n < most ? n : most;
   n = n < 1 ? 1 : n;
