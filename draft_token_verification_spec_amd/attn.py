@@ -12,12 +12,13 @@ passed as its ``transpose(1, 2)``): bfloat16, or float8_e4m3fn with ``k_scale``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import Optional
 
 import torch
 
-from . import SV_BF16, SV_F32, Workspace, _check, _load, _need
+from . import SV_BF16, SV_F32, _check, _load
 
 __all__ = [
     "SV_E4M3",
@@ -130,6 +131,12 @@ def _three(name: str, t: torch.Tensor) -> tuple:
     if len(shape) != 3:
         raise ValueError(f"{name} must be [rows, heads, head_dim] (got {list(shape)})")
     return shape
+
+
+def _new(shape: tuple, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """A contiguous [T, heads, D] tensor (torch.empty takes a third longer)."""
+    T, heads, D = shape
+    return torch.empty_strided(shape, (heads * D, D, 1), dtype=dtype, device=device)
 
 
 def _dtype_code(name: str, dtype: torch.dtype) -> int:
@@ -262,9 +269,12 @@ def sv_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, lay
     pos = _array(dev, "positions", positions, torch.int64, (T,))
     fp, rotary = _freq(dev, freq)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = _new(shape, dtype, x.device)
+        orows = out.data_ptr(), heads * D, D
+    else:
+        orows = _rows(dev, "out", out, dtype, shape)
     _call(dev, "sv_rope", T, heads, D, rotary, _layout(layout), 1 if backward else 0, code, *xr, pos, fp, mscale,
-          *_rows(dev, "out", out, dtype, shape))
+          *orows)
     return out
 
 
@@ -300,8 +310,11 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         _tensor("q", q)
         q_heads = _three("q", q)[1]
         qr = _rows(dev, "q", q, dtype, (T, q_heads, D))
-        _need(o, "q", (T, q_heads, D), dtype, q.device)
-        qo = _rows(dev, "out['q']", o["q"], dtype, (T, q_heads, D))
+        if "q" in o:
+            qo = _rows(dev, "out['q']", o["q"], dtype, (T, q_heads, D))
+        else:
+            o["q"] = _new((T, q_heads, D), dtype, q.device)
+            qo = o["q"].data_ptr(), q_heads * D, D
     _call(dev, "sv_kv_append", B, T, q_heads, code, rotary, _layout(layout), fp, mscale, pos, *qr, *qo, *kr, *vr, qs,
           kl, cache)
     return o
@@ -326,14 +339,18 @@ def sv_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     code = _dtype_code("dtype", dtype)
     o = {} if out is None else out
     shape = (rows, heads, D)
-    device = k_cache.device
-    _need(o, "k", shape, dtype, device)
-    _need(o, "v", shape, dtype, device)
-    _call(dev, "sv_kv_gather", B, rows, code, cache, rs, kb, _array(dev, "out['k']", o["k"], dtype, shape),
-          _array(dev, "out['v']", o["v"], dtype, shape))
+    ptr = []
+    for name in ("k", "v"):
+        if name in o:
+            ptr.append(_array(dev, f"out['{name}']", o[name], dtype, shape))
+        else:
+            t = o[name] = _new(shape, dtype, k_cache.device)
+            ptr.append(t.data_ptr())
+    _call(dev, "sv_kv_gather", B, rows, code, cache, rs, kb, *ptr)
     return o
 
 
+@functools.lru_cache(maxsize=4096)
 def sv_paged_attention_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int = 0,
                                       max_kv_len: int = 0) -> int:
     return int(_attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, kv_heads, head_dim, max_q_len,
@@ -344,7 +361,7 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                        query_start: torch.Tensor, kv_len: torch.Tensor, *, scale: Optional[float] = None,
                        window: int = 0, k_scale: Optional[torch.Tensor] = None,
                        v_scale: Optional[torch.Tensor] = None, max_q_len: int = 0, max_kv_len: int = 0,
-                       want_lse: bool = False, workspace: Optional[Workspace] = None,
+                       want_lse: bool = False, workspace: Optional[torch.Tensor] = None,
                        out: Optional[dict] = None) -> dict:
     """Causal attention of the new tokens ``q`` [T, q_heads, head_dim]
     (bfloat16) over a paged cache that holds them already; see
@@ -354,7 +371,8 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
 
     Without a ``workspace`` the call takes one from torch's allocator for its
     own duration: calls on different streams, and captured graphs, then share
-    nothing.  A Workspace serves one stream's calls, as everywhere."""
+    nothing.  Else a contiguous uint8 tensor of at least
+    ``sv_paged_attention_workspace_size`` bytes, used by one call at a time."""
     dev = _tensor("q", q)
     shape = T, q_heads, D = _three("q", q)
     _tensor("kv_len", kv_len)
@@ -367,18 +385,26 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     kl = _array(dev, "kv_len", kv_len, torch.int32, (B,))
     o = {} if out is None else out
     device = q.device
-    _need(o, "out", shape, torch.bfloat16, device)
-    orows = _rows(dev, "out['out']", o["out"], torch.bfloat16, shape)
-    if want_lse:
-        _need(o, "lse", (T, q_heads), torch.float32, device)
-    lse = _array(dev, "out['lse']", o["lse"], torch.float32, (T, q_heads)) if "lse" in o else None
+    if "out" in o:
+        orows = _rows(dev, "out['out']", o["out"], torch.bfloat16, shape)
+    else:
+        t = o["out"] = _new(shape, torch.bfloat16, device)
+        orows = t.data_ptr(), q_heads * D, D
+    lse = None
+    if "lse" in o:
+        lse = _array(dev, "out['lse']", o["lse"], torch.float32, (T, q_heads))
+    elif want_lse:
+        t = o["lse"] = torch.empty_strided((T, q_heads), (q_heads, 1), dtype=torch.float32, device=device)
+        lse = t.data_ptr()
     if max_kv_len == 0:
         max_kv_len = tokens
-    nbytes = _attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, heads, D, max_q_len, max_kv_len)
+    nbytes = sv_paged_attention_workspace_size(B, T, q_heads, heads, D, max_q_len, max_kv_len)
     if workspace is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     else:
-        ws = workspace.get(device, nbytes)
+        ws = workspace
+        _array(dev, "workspace", ws, torch.uint8, (ws.numel(),))
+        nbytes = ws.numel()
     _call(dev, "sv_paged_attention", B, T, q_heads, *qr, cache, qs, kl, max_q_len, max_kv_len,
-          D ** -0.5 if scale is None else scale, window, *orows, lse, ws.data_ptr(), ws.numel())
+          D ** -0.5 if scale is None else scale, window, *orows, lse, ws.data_ptr(), nbytes)
     return o

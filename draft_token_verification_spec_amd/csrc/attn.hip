@@ -858,14 +858,33 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan
   const int tok = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
   const int64_t at = blockIdx.x, all = int64_t(a.T) * a.q_heads;
   const int G = a.q_heads / c.heads;
-  const int b = uniform(find_sequence(a.query_start, a.B, tok, lane));
-  if (b < 0 || tok >= uniform_at(a.query_start, b + 1)) return;
+  // requests of equally many rows are found at once, others by a search
+  int b = int(int64_t(tok) * a.B / a.T);
+  if (tok < uniform_at(a.query_start, b) || tok >= uniform_at(a.query_start, b + 1)) {
+    b = uniform(find_sequence(a.query_start, a.B, tok, lane));
+    if (b < 0 || tok >= uniform_at(a.query_start, b + 1)) return;
+  }
   // the row's tile, as the kernel that wrote the parts saw it
   const int64_t row = int64_t(tok - uniform_at(a.query_start, b)) * G + head % G;
   const Tile t = tile_at<M>(a, G, b, uniform(int(row / M)) * int64_t(M));
   if (t.rows == 0) return;
   const Splits live = live_splits(t, p.split_len, p.num_splits);
   if (live.first == live.last) return;  // written by the split itself
+  // the first parts are asked for along with the statistics
+  constexpr int kAhead = 4;
+  const int lg = c.D <= 128 ? 5 : 6, groups = kAttnThreads >> lg;
+  const int ch = min(4 * (tid & ((1 << lg) - 1)), c.D - 4), mine = live.first + (tid >> lg);
+  auto part_at = [&](int s) {
+    return *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + ch);
+  };
+  float4 v[kAhead];
+  float m[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int s = min(mine + i * groups, live.last);
+    v[i] = part_at(s);
+    m[i] = p.part_ml[s * all + at].x;
+  }
   float top = -INFINITY;
   for (int s = live.first + lane; s <= live.last; s += 64) top = fmaxf(top, p.part_ml[s * all + at].x);
 #pragma unroll
@@ -877,17 +896,16 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan
     total = fmaf(fast_exp2(ml.x - ref), ml.y, total);
   }
   total = wave_sum(total);
-  const int lg = c.D <= 128 ? 5 : 6, groups = kAttnThreads >> lg;
-  const int ch = 4 * (tid & ((1 << lg) - 1));
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ch < c.D) {
+  auto add = [&](const float4& x, float w) {
+    y.x = fmaf(w, x.x, y.x), y.y = fmaf(w, x.y, y.y), y.z = fmaf(w, x.z, y.z), y.w = fmaf(w, x.w, y.w);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (mine + i * groups <= live.last) add(v[i], fast_exp2(m[i] - ref));
 #pragma unroll 4
-    for (int s = live.first + (tid >> lg); s <= live.last; s += groups) {
-      const float w = fast_exp2(p.part_ml[s * all + at].x - ref);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + ch);
-      y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
-    }
-  }
+  for (int s = mine + kAhead * groups; s <= live.last; s += groups)
+    add(part_at(s), fast_exp2(p.part_ml[s * all + at].x - ref));
   part[tid] = y;
   __syncthreads();
   if (tid >> lg) return;
@@ -896,7 +914,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan
     y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  if (ch < c.D)
+  if (4 * tid < c.D)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + ch) =
         make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
   if (a.lse && tid == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
@@ -950,7 +968,8 @@ void launch_dims(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
 AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len) {
   AttnPlan p;
   const int G = q_heads / kv_heads;
-  if (max_q_len <= 0 || max_q_len > T) max_q_len = B > 0 ? (T + B - 1) / B : T;
+  const int least = B > 0 ? (T + B - 1) / B : T;  // some request has that many rows
+  max_q_len = max_q_len < least ? least : max_q_len > T ? T : max_q_len;
   const int64_t rows = int64_t(max_q_len) * G;
   p.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && D <= 128 ? 64 : kManyRows;
   // a request's tiles, as far as known; workgroups go on to further ones where
@@ -965,11 +984,17 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   // of 64: 151 us filled twice, 142 us eight times; with 5 rows a head of 4096
   // 8-bit tokens each, 119 and 143 us)
   const int64_t groups = int64_t(B) * p.tiles * kv_heads;
-  const int64_t most = (int64_t(max_kv_len) + 255) / 256;
   const int64_t want = p.row_tile == 16 ? 2048 : 512;
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
-  n = n < most ? n : most;
-  n = n < 1 ? 1 : n;
+  n = n < (max_kv_len + 255) / 256 ? n : (max_kv_len + 255) / 256;
+  // With few of them one compute unit's reads are what counts (about 37 bytes a
+  // nanosecond): a workgroup for every one then, down to 128 tokens each (8
+  // heads of 1024 tokens: 8 workgroups 18.6 us, 32 of them 12.3, 64 of them
+  // 10.5).  Up to 512 tokens joining costs as much as it saves.
+  int64_t fine = groups > 0 ? 256 / groups : 1;
+  fine = fine < (max_kv_len + 127) / 128 ? fine : (max_kv_len + 127) / 128;
+  n = n > fine ? n : fine;
+  if (n < 1 || max_kv_len <= 512) n = 1;
   int64_t len = (max_kv_len + n - 1) / n;
   len = (len + 127) / 128 * 128;
   p.split_len = int(len < 128 ? 128 : len > (1 << 30) ? (1 << 30) : len);

@@ -192,6 +192,8 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  *              kv_len, as far as the caller knows them (0: not known): they
  *              choose how the work is divided and change results by rounding
  *              only; larger requests are computed all the same.
+ *   workspace  scratch of this call alone, 16-byte aligned; not a workspace of
+ *              specverify.h's calls, whose cleared part it would overwrite.
  * Scores, sums and outputs are accumulated in binary32. */
 int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
                        int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
