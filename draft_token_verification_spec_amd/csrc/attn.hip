@@ -33,6 +33,11 @@ namespace {
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kBlock = 32;  // tokens a wave takes at a time
+// Weights are taken relative to a running maximum that follows the true one only
+// when that is more than 2^8 ahead: sums and weights then stay far inside binary32
+// and bf16, and the accumulated values are rescaled in a few blocks instead of
+// in nearly all (some row of a tile has a new maximum in almost every one).
+constexpr float kSlack = 8.f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -384,24 +389,25 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[h][m][i]);
       top = max_over_quarters(top);
-      const float next = fmaxf(mx[m], top);
-      const float ref = next == -INFINITY ? 0.f : next * sc;
-      const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
-      mx[m] = next;
-      float sum = 0.f;
+      if (__any((top - mx[m]) * sc > kSlack)) {
+        const float higher = fmaxf(mx[m], top);
+        const float keep = fast_exp2((mx[m] - (higher == -INFINITY ? 0.f : higher)) * sc);
+        mx[m] = higher;
+        l[m] *= keep;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
+      }
+      const float ref = mx[m] == -INFINITY ? 0.f : mx[m] * sc;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s[h][m][i] = fast_exp2(fmaf(s[h][m][i], sc, -ref));
-          sum += s[h][m][i];
+          l[m] += s[h][m][i];
         }
-      l[m] = fmaf(l[m], keep, sum);
-      // rounded to bf16 for the product: a weight of at most 1 is off by 2^-8 of itself
+      // rounded to bf16 for the product: a weight is off by at most 2^-8 of itself
       pf[m] = make_uint4(pack_bf16(s[0][m][0], s[0][m][1]), pack_bf16(s[0][m][2], s[0][m][3]),
                          pack_bf16(s[1][m][0], s[1][m][1]), pack_bf16(s[1][m][2], s[1][m][3]));
-#pragma unroll
-      for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
     }
 #pragma unroll
     for (int d = 0; d < kDT; d += 4) {
@@ -512,6 +518,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
   constexpr int kWaveSpan = 64 / kLanes;          // and of a wave
   constexpr int kLoads = kTile / kSpan;
   constexpr int kParts = FP8 ? 2 : 1;             // 8 channels each, of a load
+  constexpr int kGroup = DP == 64 ? 2 : 4;        // products whose operands are read together
   __shared__ __align__(16) uint16_t keys[2][kTile * kPitch<DP>];
   __shared__ __align__(16) uint16_t values[2][kTile * kValuePitch<DP>];
   __shared__ __align__(16) uint8_t state[2][kTile];   // of a token: 0 present, 1 absent, 2 a value not finite
@@ -703,26 +710,26 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
-      // products in groups of four, whose operands are read a group ahead; a wave
+      // products in groups whose operands are read a group ahead; a wave
       // that has products to issue goes before one in its softmax (349 -> 343 us)
       {
         const uint16_t* const kt = &keys[buf][r * kPitch<DP> + 8 * h];
-        uint4 kf[2][4];
+        uint4 kf[2][kGroup];
         auto read = [&](int n) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            kf[(n >> 2) & 1][i] =
+          for (int i = 0; i < kGroup; ++i)
+            kf[n / kGroup & 1][i] =
                 *reinterpret_cast<const uint4*>(kt + 32 * ((n + i) & 1) * kPitch<DP> + 16 * ((n + i) >> 1));
         };
         read(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int n = 0; n < 2 * kSteps; n += 4) {
-          if (n + 4 < 2 * kSteps) read(n + 4);
+        for (int n = 0; n < 2 * kSteps; n += kGroup) {
+          if (n + kGroup < 2 * kSteps) read(n + kGroup);
           keep_order();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[(n + i) & 1] = mfma32(kf[(n >> 2) & 1][i], qf[(n + i) >> 1], s[(n + i) & 1]);
+          for (int i = 0; i < kGroup; ++i)
+            s[(n + i) & 1] = mfma32(kf[n / kGroup & 1][i], qf[(n + i) >> 1], s[(n + i) & 1]);
           keep_order();
         }
       }
@@ -750,7 +757,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
       top = max_over_halves(top);
-      if (__any(top > mx)) {
+      if (__any((top - mx) * sc > kSlack)) {
         const float higher = fmaxf(mx, top);
         const float keep = fast_exp2((mx - (higher == -INFINITY ? 0.f : higher)) * sc);
         mx = higher;
@@ -761,14 +768,14 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       const float ref = mx == -INFINITY ? 0.f : mx * sc;
       const uint16_t* const vt =
           &values[buf][(4 * h + ((lane & 15) >> 2)) * kValuePitch<DP> + (lane & 16) + 4 * (lane & 3)];
-      uint4 vf[2][4];
+      uint4 vf[2][kGroup];
       auto read_values = [&](int n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kGroup; ++i) {
           const int at = n + i, d = at % kDT, t16 = at / kDT;  // channels 32 d .., tokens 16 t16 ..
           const uint2 v0 = read_transposed(vt + 16 * t16 * kValuePitch<DP> + 32 * d);
           const uint2 v1 = read_transposed(vt + (16 * t16 + 8) * kValuePitch<DP> + 32 * d);
-          vf[(n >> 2) & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+          vf[n / kGroup & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
         }
       };
       read_values(0);
@@ -780,7 +787,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
           s[u][i] = fast_exp2(fmaf(s[u][i], sc, -ref));
           l += s[u][i];
         }
-        // rounded to bf16 for the product: a weight of at most 1 is off by 2^-8 of itself
+        // rounded to bf16 for the product: a weight is off by at most 2^-8 of itself
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           pf[u][q] = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
@@ -789,13 +796,13 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       }
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int n = 0; n < 4 * kDT; n += 4) {
-        if (n + 4 < 4 * kDT) read_values(n + 4);
+      for (int n = 0; n < 4 * kDT; n += kGroup) {
+        if (n + kGroup < 4 * kDT) read_values(n + kGroup);
         keep_order();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kGroup; ++i) {
           const int at = n + i, d = at % kDT, t16 = at / kDT;
-          o[d] = mfma32(vf[(n >> 2) & 1][i], pf[t16 >> 1][t16 & 1], o[d]);
+          o[d] = mfma32(vf[n / kGroup & 1][i], pf[t16 >> 1][t16 & 1], o[d]);
         }
         keep_order();
       }
