@@ -271,3 +271,91 @@ def test_attention_empty_and_refusals():
         sv.sv_paged_attention(*swap(0, flat[4:].view(4, 8, 64)))  # 8-byte aligned
     with pytest.raises(ValueError):
         sv.sv_paged_attention(*a, out=dict(out=q[:3]))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 16, 32, 64, 1024])
+@pytest.mark.parametrize("new,total,heads,q_heads,D", [
+    ([1, 3], [70, 200], 2, 8, 128), ([10, 2], [150, 44], 1, 4, 64), ([13], [90], 2, 6, 128), ([30], [77], 1, 1, 256),
+    ([70, 5], [90, 170], 1, 2, 128), ([140], [150], 2, 2, 64), ([40], [140], 1, 4, 256),
+])
+def test_attention_page_sizes(cache, page, new, total, heads, q_heads, D):
+    """Every kernel (16, 32, 64 and 128 rows) with pages from one token to more than the context."""
+    pages, table, start = tables(new, total, page, seed=page)
+    c = fill(new_cache(cache, pages, page, heads, D), page)
+    q = torch.randn((start[-1], q_heads, D), device="cuda").bfloat16()
+    o = call(q, c, table, start, total, max_q_len=max(new), max_kv_len=max(total))
+    check(o, q, c, table, start, total, D ** -0.5)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,total,window,q_heads", [
+    ([3], [3000], 0, 4), ([3], [3000], 700, 4), ([9, 1], [2600, 30], 0, 8), ([20], [2900], 1000, 4),
+    ([60, 2], [2100, 1800], 0, 4), ([50], [4000], 300, 4), ([1, 1, 1], [5000, 700, 0], 0, 2),
+])
+def test_attention_long_contexts_in_splits(cache, new, total, window, q_heads):
+    """Contexts that are divided, windows that begin in a later split, requests that need none of the splits."""
+    pages, table, start = tables(new, total, 32, seed=len(new))
+    c = fill(new_cache(cache, pages, 32, 1, 128), 7)
+    q = torch.randn((start[-1], q_heads, 128), device="cuda").bfloat16()
+    size = sv.sv_paged_attention_workspace_size(len(new), int(start[-1]), q_heads, 1, 128, max(new), max(total))
+    assert size > 256
+    o = call(q, c, table, start, total, window=window, max_q_len=max(new), max_kv_len=max(total))
+    check(o, q, c, table, start, total, 128 ** -0.5, window)
+
+
+@pytest.mark.parametrize("q_heads", [2, 16])
+def test_attention_of_one_long_request_among_short_ones(q_heads):
+    """A request with far more rows than the average (and than a wrong hint says): its workgroups go on to its other
+    tiles."""
+    new, total = [1, 300, 1, 0, 2, 1, 1, 1], [40, 310, 1, 9, 77, 500, 3, 64]
+    pages, table, start = tables(new, total, 16)
+    c = fill(new_cache("bf16", pages, 16, 2, 64), 1)
+    q = torch.randn((start[-1], q_heads, 64), device="cuda").bfloat16()
+    for kw in ({}, dict(max_q_len=1), dict(max_q_len=300), dict(max_kv_len=3)):
+        o = call(q, c, table, start, total, **kw)
+        check(o, q, c, table, start, total, 0.125)
+
+
+def test_attention_of_keys_and_values_in_one_tensor():
+    """Keys and values interleaved in one allocation, and a cache with more heads' room than it has."""
+    new, total, page, D = [3, 40], [60, 64], 16, 128
+    pages, table, start = tables(new, total, page)
+    for view in (lambda t: (t[:, 0], t[:, 1]), lambda t: (t[:, 0, :, 1:3], t[:, 1, :, :2])):
+        both = torch.randn((pages, 2, page, 4, D), device="cuda").bfloat16()
+        k, v = view(both)
+        heads = k.shape[2]
+        c = dict(k_cache=k, v_cache=v, k_scale=None, v_scale=None)
+        x = torch.randn((43, heads, D), device="cuda").bfloat16()
+        sv.sv_kv_append(x, -x, k, v, I32(table), I32(start), I32(total))
+        q = torch.randn((43, 2 * heads, D), device="cuda").bfloat16()
+        o = call(q, c, table, start, total)
+        check(o, q, c, table, start, total, D ** -0.5)
+        back = sv.sv_kv_gather(k, v, I32(table), I32(start), 43, kv_begin=I32([57, 24]))
+        assert torch.equal(back["k"], x) and torch.equal(back["v"], -x)
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_attention_of_many_heads(new):
+    """1024 query heads over 512 and over one key head."""
+    for heads in (512, 1):
+        pages, table, start = tables([new], [60], 16)
+        c = fill(new_cache("bf16", pages, 16, heads, 16), 1)
+        q = torch.randn((new, 1024, 16), device="cuda").bfloat16()
+        o = call(q, c, table, start, [60])
+        check(o, q, c, table, start, [60], 0.25)
+
+
+@pytest.mark.parametrize("new,q_heads", [(1, 4), (12, 4), (140, 2)])
+def test_attention_of_queries_that_are_not_finite(new, q_heads):
+    """A row's queries reach that row alone."""
+    pages, table, start = tables([new], [200], 16)
+    c = fill(new_cache("bf16", pages, 16, 1, 128), 1)
+    q = torch.randn((new, q_heads, 128), device="cuda").bfloat16()
+    clean = call(q, c, table, start, [200])
+    q[new // 2, 1, 5] = float("nan")
+    o = call(q, c, table, start, [200])
+    hit = torch.zeros((new, q_heads), dtype=torch.bool, device="cuda")
+    hit[new // 2, 1] = True
+    assert torch.isnan(o["out"][hit]).all() and torch.isnan(o["lse"][hit]).all()
+    assert torch.equal(o["out"][~hit], clean["out"][~hit]) and torch.equal(o["lse"][~hit], clean["lse"][~hit])
