@@ -66,6 +66,8 @@ _SIGNATURES = {
 }
 
 _lib = None
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (missing where torch has no device support)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _attn_lib():
@@ -218,18 +220,13 @@ def _paged(dev: int, B: int, k_cache, v_cache, page_table, k_scale, v_scale):
         max_pages * page_size
 
 
-def _stream_of(dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
 def _call(dev: int, what: str, *args):
     """Call the C entry point on the device's current stream, with the device current."""
-    fn = getattr(_lib or _attn_lib(), what)
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(_stream_of(dev), *args)
+    if _current_device() == dev:
+        status = getattr(_lib or _attn_lib(), what)(_stream_of(dev), *args)
     else:
         with torch.cuda.device(dev):
-            status = fn(_stream_of(dev), *args)
+            status = getattr(_lib or _attn_lib(), what)(_stream_of(dev), *args)
     if status != 0:
         _check(status, what)
 
@@ -399,12 +396,14 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if max_kv_len == 0:
         max_kv_len = tokens
     nbytes = sv_paged_attention_workspace_size(B, T, q_heads, heads, D, max_q_len, max_kv_len)
+    ws = None
     if workspace is None:
-        ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
+        if nbytes > 256:
+            ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     else:
         ws = workspace
         _array(dev, "workspace", ws, torch.uint8, (ws.numel(),))
         nbytes = ws.numel()
     _call(dev, "sv_paged_attention", B, T, q_heads, *qr, cache, qs, kl, max_q_len, max_kv_len,
-          D ** -0.5 if scale is None else scale, window, *orows, lse, ws.data_ptr(), nbytes)
+          D ** -0.5 if scale is None else scale, window, *orows, lse, None if ws is None else ws.data_ptr(), nbytes)
     return o

@@ -243,7 +243,9 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
     if (s < 0 || s % 8 != 0) return SV_ERR_INVALID_ARG;
   if (!write_strides_ok(T, q_heads, cache->head_dim, out_token_stride, out_head_stride)) return SV_ERR_INVALID_ARG;
   AttnPlan p = plan_attention(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < 256 + p.ml_bytes + p.o_bytes) return SV_ERR_WORKSPACE;
+  if (p.num_splits > 1 &&
+      (!workspace || !aligned16(workspace) || workspace_bytes < 256 + p.ml_bytes + p.o_bytes))
+    return SV_ERR_WORKSPACE;
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
   AttnArgs a;

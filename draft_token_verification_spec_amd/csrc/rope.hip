@@ -166,10 +166,15 @@ template <bool VEC, bool FP8, typename ET>
 __global__ __launch_bounds__(kRopeThreads) void append_kernel(AppendArgs a) {
   __shared__ float2 cs[kMaxPairs];
   const int t = blockIdx.x;
-  const int b = find_sequence(a.query_start, a.B, t, threadIdx.x & 63);
-  if (b < 0) return;
-  const int end = a.query_start[b + 1];
-  if (t >= end) return;  // behind the last sequence
+  // requests of equally many rows are found at once, others by a search
+  int b = int(int64_t(t) * a.B / a.T);
+  int end = a.query_start[b + 1];
+  if (t < a.query_start[b] || t >= end) {
+    b = find_sequence(a.query_start, a.B, t, threadIdx.x & 63);
+    if (b < 0) return;
+    end = a.query_start[b + 1];
+    if (t >= end) return;  // behind the last request
+  }
   const int place = max(a.kv_len[b], 0) - (end - t);
   const int page = page_of(a.cache, b, place);
   const double position = a.positions ? double(a.positions[t]) : double(place);

@@ -167,8 +167,8 @@ int sv_kv_append(void* stream, int B, int T, int q_heads, int dtype, int rotary_
 int sv_kv_gather(void* stream, int B, int T, int out_dtype, const sv_paged_cache* cache, const int32_t* row_start,
                  const int32_t* kv_begin, void* k_out, void* v_out);
 
-/* Bytes of workspace that sv_paged_attention needs for these sizes (at least
- * 256; it grows with T and max_kv_len where long contexts are split), or 0 for
+/* Bytes of workspace that sv_paged_attention needs for these sizes: 256 stands
+ * for none (no context is split; the call then takes a NULL workspace), 0 for
  * sizes that the call would reject. */
 size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim, int max_q_len,
                                          int max_kv_len);

@@ -210,8 +210,8 @@ def test_gather_refuses_before_launch(kw, status):
     (dict(q_heads=1026), -2), (dict(q=None), -1), (dict(q=FAKE + 8), -1), (dict(out=None), -1), (dict(out=FAKE + 2), -1),
     (dict(qt=250), -1), (dict(qh=4), -1), (dict(ot=-8), -1), (dict(ot=0), -1), (dict(oh=32), -1), (dict(qs=None), -1),
     (dict(kl=None), -1), (dict(max_q=-1), -1), (dict(max_kv=-1), -1), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
-    (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(window=-1), -1), (dict(ws=None), -3),
-    (dict(ws=FAKE + 4), -3), (dict(bytes=8), -3), (dict(T=0, q=None), 0), (dict(B=0, q=None), 0),
+    (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(window=-1), -1), (dict(ws=None, max_kv=5000), -3),
+    (dict(ws=FAKE + 4, max_kv=5000), -3), (dict(bytes=8, max_kv=5000), -3), (dict(T=0, q=None), 0), (dict(B=0, q=None), 0),
 ])
 def test_attention_refuses_before_launch(kw, status):
     assert attention(**kw) == status
@@ -224,7 +224,8 @@ def test_missing_cache_is_refused():
 
 def test_attention_workspace_size():
     size = sv.sv_paged_attention_workspace_size
-    assert size(4, 20, 32, 8, 128, 5, 1000) >= 256
+    assert size(4, 20, 32, 8, 128, 5, 300) == 256  # no context is split: no workspace is needed
+    assert size(4, 20, 32, 8, 128, 5, 5000) > 256 + 20 * 32 * 128 * 4
     assert size(0, 0, 32, 8, 128) >= 256
     for bad in ((-1, 20, 32, 8, 128), (4, -1, 32, 8, 128), (4, 20, 30, 8, 128), (4, 20, 32, 0, 128), (4, 20, 32, 8, 24),
                 (4, 20, 32, 8, 512), (4, 20, 2048, 8, 128)):
