@@ -13,7 +13,7 @@
 // product's inner dimension is free as long as both operands agree).  Only
 // V^T needs its elements transposed, which the transposing LDS reads do.
 //
-// Few rows (up to 64 a request and head): HBM-bound.  The four waves take
+// Few rows (up to 32 a request and head): HBM-bound.  The four waves take
 // blocks of 32 tokens in turn, each with its own running statistics, so that
 // no wave waits for another until their results are joined at the end; keys go
 // from memory to registers directly in the A operand's layout (a lane's 16
@@ -172,7 +172,7 @@ constexpr int kValuePitch = DP + 16;
 // offset within 16 tokens): every lane looks its token's page up.  Otherwise 16
 // tokens lie in one page, whose address is scalar.
 template <int DP, int MT, bool FP8, bool SMALL>
-__global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP * MT >= 128 ? 2 : 3) void few_rows_kernel(
+__global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 3) void few_rows_kernel(
     AttnArgs a, AttnPlan p) {
   constexpr int M = 16 * MT;
   constexpr int kSteps = DP / 32;        // of the score product
@@ -439,20 +439,22 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
   asm volatile("" : "+v"(tid));  // (what follows from it is formed here, not kept in registers through the loop)
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
+    if (16 * m >= t.rows) break;
     const int row = 16 * m + r;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][row]);
     const float ref = top == -INFINITY ? 0.f : top * sc;
     const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
-    float* part = reinterpret_cast<float*>(values[wave]);  // [16][DP] as channels by rows
+    // rows of DP channels and 16 bytes more, which keep 8 rows' stores apart
+    float* part = reinterpret_cast<float*>(values[wave]) + r * (DP + 4) + 4 * g;
 #pragma unroll
     for (int d = 0; d < kDT; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[(16 * d + 4 * g + i) * 16 + r] = o[d][m][i] * keep;
+      *reinterpret_cast<float4*>(part + 16 * d) =
+          make_float4(o[d][m][0] * keep, o[d][m][1] * keep, o[d][m][2] * keep, o[d][m][3] * keep);
     __syncthreads();
     // 16 rows by 16 threads, 8 channels at a time
-    const int orow = tid & 15;
+    const int orow = tid >> 4;
     const int trow = 16 * m + orow;
     if (trow < t.rows) {
       float rtop = -INFINITY, total = 0.f;
@@ -464,22 +466,25 @@ __global__ __launch_bounds__(kAttnThreads, DP * MT > 256 || DP == 256 ? 1 : DP *
       const int tok = t.token0 + (t.first_row + trow) / G, head = kvh * G + (t.first_row + trow) % G;
       const int64_t at = int64_t(tok) * a.q_heads + head;
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      for (int ch = tid >> 4; ch < chunks; ch += 16) {
-        float y[8];
+      for (int ch = tid & 15; ch < chunks; ch += 16) {
+        float y[8] = {};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          y[j] = 0.f;
+        for (int w = 0; w < kAttnWaves; ++w) {
+          float x[8];
+          load8(reinterpret_cast<const float*>(values[w]) + orow * (DP + 4) + 8 * ch, x);
 #pragma unroll
-          for (int w = 0; w < kAttnWaves; ++w)
-            y[j] += reinterpret_cast<const float*>(values[w])[(8 * ch + j) * 16 + orow];
-          if (alone) y[j] *= inv;
+          for (int j = 0; j < 8; ++j) y[j] += x[j];
+        }
+        if (alone) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] *= inv;
         }
         if (alone)
           store8(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + 8 * ch, y);
         else
           store8(p.part_o + (split * (int64_t(a.T) * a.q_heads) + at) * c.D + 8 * ch, y);
       }
-      if (tid < 16) {
+      if ((tid & 15) == 0) {
         if (!alone)
           p.part_ml[split * (int64_t(a.T) * a.q_heads) + at] = make_float2(rtop == -INFINITY ? rtop : rref, total);
         else if (a.lse)
@@ -567,6 +572,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
     const int first_place = t.place0 + t.first_row / G;
     const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
     const float sc = a.scale * kLog2e;
+    const bool busy = 32 * wave < t.rows;
 
     f32x16 o[kDT];
 #pragma unroll
@@ -705,6 +711,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       const int next = base + kTile;
       request(next, c.k, c.ku, c.k_scale, kin, kscale);
       request(next, c.v, c.vu, c.v_scale, vin, vscale);
+      if (busy) {  // (a wave without rows only helps to load)
       f32x16 s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -807,6 +814,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
         keep_order();
       }
       __builtin_amdgcn_s_setprio(0);
+      }
       stage_keys(buf ^ 1);
       stage_values(next, buf ^ 1);
       pages(next + kTile);
@@ -947,7 +955,7 @@ void launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     launch_few<DP, 1, FP8, SMALL>(a, p, grid, stream);
   } else if (p.row_tile == 32) {
     launch_few<DP, 2, FP8, SMALL>(a, p, grid, stream);
-  } else if (p.row_tile == kManyRows) {
+  } else {
     if (SMALL)
       hipLaunchKernelGGL((many_rows_kernel<DP, FP8, 0>), grid, dim3(kAttnThreads), 0, stream, a, p);
     else if (a.cache.page_shift < 6)
@@ -955,8 +963,6 @@ void launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     else
       hipLaunchKernelGGL((many_rows_kernel<DP, FP8, 2>), grid, dim3(kAttnThreads), 0, stream, a, p);
     launch_join<kManyRows>(a, p, stream);
-  } else if constexpr (DP < 256) {
-    launch_few<DP, 4, FP8, SMALL>(a, p, grid, stream);
   }
 }
 
@@ -978,7 +984,7 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   const int least = B > 0 ? (T + B - 1) / B : T;  // some request has that many rows
   max_q_len = max_q_len < least ? least : max_q_len > T ? T : max_q_len;
   const int64_t rows = int64_t(max_q_len) * G;
-  p.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && D <= 128 ? 64 : kManyRows;
+  p.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : kManyRows;
   // a request's tiles, as far as known; workgroups go on to further ones where
   // a request has more
   int64_t tiles = (rows + p.row_tile - 1) / p.row_tile;
