@@ -389,8 +389,9 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[h][m][i]);
       top = max_over_quarters(top);
-      if (__any((top - mx[m]) * sc > kSlack)) {
-        const float higher = fmaxf(mx[m], top);
+      const bool ahead = (top - mx[m]) * sc > kSlack;
+      if (__any(ahead)) {
+        const float higher = ahead ? top : mx[m];  // (one row's scores change no other row's roundings)
         const float keep = fast_exp2((mx[m] - (higher == -INFINITY ? 0.f : higher)) * sc);
         mx[m] = higher;
         l[m] *= keep;
@@ -764,8 +765,9 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
       top = max_over_halves(top);
-      if (__any((top - mx) * sc > kSlack)) {
-        const float higher = fmaxf(mx, top);
+      const bool ahead = (top - mx) * sc > kSlack;
+      if (__any(ahead)) {
+        const float higher = ahead ? top : mx;  // (one row's scores change no other row's roundings)
         const float keep = fast_exp2((mx - (higher == -INFINITY ? 0.f : higher)) * sc);
         mx = higher;
         l *= keep;

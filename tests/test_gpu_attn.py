@@ -359,3 +359,24 @@ def test_attention_of_queries_that_are_not_finite(new, q_heads):
     hit[new // 2, 1] = True
     assert torch.isnan(o["out"][hit]).all() and torch.isnan(o["lse"][hit]).all()
     assert torch.equal(o["out"][~hit], clean["out"][~hit]) and torch.equal(o["lse"][~hit], clean["lse"][~hit])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,q_heads,total", [(4, 4, 900), (8, 4, 300), (8, 4, 320), (160, 2, 704), (320, 1, 1344)])
+@pytest.mark.parametrize("seed", range(3))
+def test_attention_of_a_row_keeps_its_bits_when_a_later_token_changes(cache, new, q_heads, total, seed):
+    """Also where the later rows of its tile see a score far above all others."""
+    pages, table, start = tables([new], [total], 16, seed=new)
+    c = fill(new_cache(cache, pages, 16, 1, 128), new + seed)
+    g = torch.Generator(device="cuda").manual_seed(new + seed)
+    q = torch.randn((new, q_heads, 128), generator=g, device="cuda").bfloat16()
+    kw = dict(max_q_len=new, max_kv_len=total, scale=0.05)
+    a = call(q, c, table, start, [total], **kw)
+    page, slot = int(table[0][(total - 1) // 16]), (total - 1) % 16
+    key = c["k_cache"][page, slot, 0]
+    key.copy_((q[-1, 0].float() * 100).to(key.dtype))
+    b = call(q, c, table, start, [total], **kw)
+    for n in ("out", "lse"):
+        assert torch.equal(a[n][:-1], b[n][:-1]), n
+        assert not torch.equal(a[n][-1], b[n][-1]), n
+    check(b, q, c, table, start, [total], 0.05)
