@@ -239,8 +239,10 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
   if (!(scale > 0.f) || !isfinite(scale) || window < 0) return SV_ERR_INVALID_ARG;
   if (empty) return SV_OK;
   if (!q || !out || !query_start || !kv_len || !aligned16(q) || !aligned16(out)) return SV_ERR_INVALID_ARG;
-  for (int64_t s : {q_token_stride, q_head_stride, out_token_stride, out_head_stride})
-    if (s < 0 || s % 8 != 0) return SV_ERR_INVALID_ARG;
+  for (int64_t s : {q_token_stride, out_token_stride})
+    if (s < 0 || (T > 1 && s % 8 != 0)) return SV_ERR_INVALID_ARG;
+  for (int64_t s : {q_head_stride, out_head_stride})
+    if (s < 0 || (q_heads > 1 && s % 8 != 0)) return SV_ERR_INVALID_ARG;
   if (!write_strides_ok(T, q_heads, cache->head_dim, out_token_stride, out_head_stride)) return SV_ERR_INVALID_ARG;
   AttnPlan p = plan_attention(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
   if (p.num_splits > 1 &&

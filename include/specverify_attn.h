@@ -182,10 +182,13 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  * A row that sees no token gets out = 0 and lse = -infinity.  A token that a
  * row does not see has no influence on it, whatever its key and value hold.  A
  * NaN that a row sees shows: one in a key makes its whole result NaN, one in a
- * value the channel's at least.
+ * value the channel's at least.  An infinite value that a row sees makes the
+ * channel's result infinite or NaN, and may make the row's others and its lse
+ * NaN.
  *   q, out     SV_BF16 elements, [T, q_heads, head_dim] with the given
- *              strides, 16-byte aligned, strides multiples of 8 elements;
- *              q_heads a multiple of cache->heads.
+ *              strides, 16-byte aligned, strides multiples of 8 elements (that
+ *              of a dimension of one element is not looked at); no two of
+ *              out's rows may overlap.  q_heads a multiple of cache->heads.
  *   lse        float [T, q_heads], or NULL.
  *   scale      > 0 and finite (usually head_dim^-0.5).
  *   max_q_len, max_kv_len   the most new tokens of a request and the largest

@@ -380,3 +380,16 @@ def test_attention_of_a_row_keeps_its_bits_when_a_later_token_changes(cache, new
         assert torch.equal(a[n][:-1], b[n][:-1]), n
         assert not torch.equal(a[n][-1], b[n][-1]), n
     check(b, q, c, table, start, [total], 0.05)
+
+
+def test_attention_strides_of_dimensions_of_one():
+    pages, table, start = tables([1], [70], 16, seed=1)
+    c = fill(new_cache("bf16", pages, 16, 1, 64), 1)
+    q = torch.randn((1, 4, 64), device="cuda").bfloat16()
+    odd = lambda x: torch.as_strided(x, x.shape, (777, x.stride(1), 1))
+    out = dict(out=odd(torch.zeros_like(q)))
+    o = call(odd(q), c, table, start, [70], out=out)
+    check(o, q, c, table, start, [70], 0.125)
+    q1 = torch.randn((1, 1, 64), device="cuda").bfloat16()
+    o = call(torch.as_strided(q1, (1, 1, 64), (777, 5, 1)), c, table, start, [70])
+    check(o, q1, c, table, start, [70], 0.125)
