@@ -85,7 +85,8 @@ int check_attention_sizes(int B, int T, int q_heads, int kv_heads, int head_dim,
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 16 || head_dim % 16 != 0 ||
       max_q_len < 0 || max_kv_len < 0)
     return SV_ERR_INVALID_ARG;
-  if (q_heads > SV_ATTN_MAX_HEADS || head_dim > SV_ATTN_MAX_HEAD_DIM) return SV_ERR_UNSUPPORTED;
+  if (q_heads > SV_ATTN_MAX_HEADS || head_dim > SV_ATTN_MAX_HEAD_DIM || int64_t(T) * q_heads > INT32_MAX)
+    return SV_ERR_UNSUPPORTED;  // (a request's rows times heads are counted in 32 bits)
   return SV_OK;
 }
 

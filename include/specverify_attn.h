@@ -188,7 +188,8 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  *   q, out     SV_BF16 elements, [T, q_heads, head_dim] with the given
  *              strides, 16-byte aligned, strides multiples of 8 elements (that
  *              of a dimension of one element is not looked at); no two of
- *              out's rows may overlap.  q_heads a multiple of cache->heads.
+ *              out's rows may overlap.  q_heads a multiple of cache->heads,
+ *              T * q_heads below 2^31.
  *   lse        float [T, q_heads], or NULL.
  *   scale      > 0 and finite (usually head_dim^-0.5).
  *   max_q_len, max_kv_len   the most new tokens of a request and the largest

@@ -245,3 +245,10 @@ def test_binding_refuses_host_tensors():
         sv.sv_kv_gather(c, c, i(1, 2), i(2), 3)
     with pytest.raises(ValueError, match="HIP device"):
         sv.sv_paged_attention(x, c, c, i(1, 2), i(2), i(1))
+
+
+def test_attention_rows_and_heads_stay_within_32_bits():
+    """A request's rows times its query heads are counted in 32 bits."""
+    assert attention(T=1 << 23, q_heads=256, max_kv=100) == -2
+    assert sv.sv_paged_attention_workspace_size(4, 1 << 23, 256, 2, 64) == 0
+    assert sv.sv_paged_attention_workspace_size(4, (1 << 23) - 1, 256, 2, 64) >= 256
