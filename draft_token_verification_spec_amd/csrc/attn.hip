@@ -3,23 +3,47 @@
 // For a request b and key / value head kvh, the n new tokens and the
 // G = q_heads / heads query heads of the group make R = n * G rows that read
 // the same keys and values: row r is token r / G, head kvh * G + r % G.  A
-// workgroup takes a tile of kRowTile rows and a range of tokens (a split).
+// workgroup takes a tile of rows and a range of tokens (a split) and forms, for
+// a row with scores x_j = scale q . k_j,
+//   l = sum_j exp(x_j - m),   o = sum_j exp(x_j - m) v_j,   out = o / l,
+// in one pass over the tokens with a running reference m near the maximum.
 //
 // Scores are formed transposed, S^T = K Q^T, so that a lane of the matrix
-// instruction's result holds one row (lane & 15) and four tokens: the softmax
+// instruction's result holds one row and several tokens: the softmax
 // statistics of a row are one value per lane, its running maximum a reduction
-// inside the lane and over the four lanes of the row, and the weights are
-// already the B operand of O^T += V^T P^T (the order of the tokens inside a
-// product's inner dimension is free as long as both operands agree).  Only
-// V^T needs its elements transposed, which the transposing LDS reads do.
+// inside the lane and over the lanes of the row, and the weights are already
+// the B operand of O^T += V^T P^T (the order of the tokens inside a product's
+// inner dimension is free as long as both operands agree).  Only V^T needs its
+// elements transposed, which the transposing LDS reads do.
 //
-// Few rows (up to 32 a request and head): HBM-bound.  The four waves take
-// blocks of 32 tokens in turn, each with its own running statistics, so that
-// no wave waits for another until their results are joined at the end; keys go
-// from memory to registers directly in the A operand's layout (a lane's 16
-// bytes of one token's row), values through the wave's own part of LDS.  A
-// wave asks for the next block's keys and values as soon as the present ones
-// have left their registers.
+// Few rows (up to 32 a request and head: decoding, verification of drafts):
+// HBM-bound. The four waves take blocks of 32 tokens in turn, each with its
+// own running statistics, so that no wave waits for another until their
+// results are joined at the end; keys go from memory to registers directly in
+// the A operand's layout (a lane's 16 bytes of one token's row), values
+// through the wave's own part of LDS. A wave asks for the next block's keys
+// and values as soon as the present ones have left their registers. Measured:
+// 64 requests of 1024 to 4096 bf16 tokens, 8 heads of 128 channels, 677 MB
+// read in 136 us (5.0 TB/s, of which the paged rows alone read at 6.1 in a
+// kernel that only loads); 256 requests of 500 to 2000 8-bit tokens, 5 new
+// tokens of 4 heads for each of 8, 689 MB in 149 us (4.6 TB/s). What is
+// missing to the read rate: a workgroup's start and end (5 to 7 us each, in
+// which its compute unit slot asks for nothing) and the uneven lengths at the
+// end of the grid.
+//
+// Many rows (chunks of a prompt): bound by the softmax's vector instructions
+// and by LDS, both beside the products. The four waves have 32 rows each and
+// share tiles of 64 tokens, loaded a tile ahead into registers and staged in
+// two LDS buffers, so that a tile is read from memory once for 128 rows.
+// Measured: 2048 new tokens behind 8192, 32 heads of 128 channels over 8: 309
+// GFLOP in 323 to 334 us, 925 to 956 TFLOP/s (a library product of two 4096 x
+// 4096 matrices: 1087); packed prompts of up to 4000 tokens at 64 channels
+// with a window of 2048, where a product has half the work for each
+// exponential: 580 to 596 TFLOP/s. With a tile of rows a request it is
+// HBM-bound as well: 9 new tokens of 8 heads for each of 4 behind 131071, 4
+// requests, 1.07 GB in 211 us (5.1 TB/s). 32 rows of 256 channels are as fast
+// in either kernel for bf16 (72.8 and 74.9 us, 16 requests of 2048 tokens),
+// but not for 8-bit caches (46.8 and 67.0 us).
 //
 // Splits: where rows are few and contexts long, a context is divided into
 // ranges of `split_len` tokens, whose results (running maximum, sum, weighted
@@ -36,7 +60,8 @@ constexpr int kBlock = 32;  // tokens a wave takes at a time
 // Weights are taken relative to a running maximum that follows the true one only
 // when that is more than 2^8 ahead: sums and weights then stay far inside binary32
 // and bf16, and the accumulated values are rescaled in a few blocks instead of
-// in nearly all (some row of a tile has a new maximum in almost every one).
+// in nearly all (some row of a tile has a new maximum in almost every one):
+// 2048 new tokens behind 8192 344 -> 334 us, packed prompts 211 -> 202 us.
 constexpr float kSlack = 8.f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -62,7 +87,7 @@ __device__ __forceinline__ uint4 load_from(const char* p, uint32_t at) {
 // the same request for every head and split, and requests of different lengths
 // load the XCDs unevenly: blocks of 8 positions are turned by one from head to
 // head and from split to split (a decoding batch of 64 at 1024 to 4096 tokens:
-// 155 -> 142 us).
+// 156 -> 141 us).
 __device__ __forceinline__ uint32_t spread_over_xcds(uint32_t x, uint32_t head, uint32_t split) {
   if ((x | 7u) >= gridDim.x) return x;
   const uint32_t turn = ((gridDim.x & 1u) ? 0u : head) + ((gridDim.x & gridDim.y & 1u) ? 0u : split);
@@ -189,311 +214,311 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
   const int at_x = spread_over_xcds(blockIdx.x, kvh, split);
   const int b = at_x / p.tiles;
   for (int64_t first_row = int64_t(at_x - b * p.tiles) * M;; first_row += int64_t(p.tiles) * M) {
-  const Tile t = tile_at<M>(a, G, b, first_row);
-  if (t.rows == 0) return;
-  const Splits live = live_splits(t, p.split_len, p.num_splits);
-  if (split < live.first || split > live.last) continue;
-  const int begin = max(t.begin, split * p.split_len) & ~(kBlock - 1);
-  const int end = split == p.num_splits - 1 ? t.end : min(t.end, (split + 1) * p.split_len);
+    const Tile t = tile_at<M>(a, G, b, first_row);
+    if (t.rows == 0) return;
+    const Splits live = live_splits(t, p.split_len, p.num_splits);
+    if (split < live.first || split > live.last) continue;
+    const int begin = max(t.begin, split * p.split_len) & ~(kBlock - 1);
+    const int end = split == p.num_splits - 1 ? t.end : min(t.end, (split + 1) * p.split_len);
 
-  // queries: the B operand, lane (row, g) holding the channels of its steps
-  const int chunks = c.D >> 3;
-  uint4 qf[MT][kSteps];
-  int place[MT], oldest[MT];  // of the lane's rows: they see the tokens oldest < j <= place
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = 16 * m + r;
-    const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
-    place[m] = row < t.rows ? t.place0 + tok : -1;
-    oldest[m] = a.window > 0 ? max(place[m], -1) - a.window : -1;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int ch = FP8 ? 8 * (s >> 1) + 2 * g + (s & 1) : 4 * s + g;
-      qf[m][s] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < t.rows && ch < chunks) qf[m][s] = *reinterpret_cast<const uint4*>(q + 8 * ch);
-    }
-  }
-  const int first_place = t.place0 + t.first_row / G;  // the places of the tile's first and last rows
-  const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
-  const float sc = a.scale * kLog2e;
-
-  f32x4 o[kDT][MT];
-  float mx[MT], l[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mx[m] = -INFINITY;
-    l[m] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kDT; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  uint4 kr[2][kLoads], vr[2][kLoads];
-  uint32_t ks[2] = {127, 127}, vs[2] = {127, 127};
-  bool have[2];
-  const int64_t table = b * c.table_stride;
-  const int in_page = (1 << c.page_shift) - 1;
-  // the page table's entries of the block's tokens 0 .. 15 and 16 .. 31 (SMALL:
-  // of this lane's, r and 16 + r), or of the last token in their place
-  int page[2];
-  auto pages = [&](int base) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = min(base + 16 * h + (SMALL ? r : 0), end - 1);
-      page[h] = SMALL ? c.table[table + (j >> c.page_shift)] : uniform_at(c.table, table + (j >> c.page_shift));
-    }
-  };
-  // ask for a block's rows; the loads of absent tokens and of channels beyond
-  // the head's go to page 0 and to its last channels, and are not used
-  uint32_t lane_at[2][kLoads];  // bytes from the 16 tokens' first row, of keys and of values
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const uint32_t unit = min(4 * i + g, (FP8 ? c.D >> 4 : c.D >> 3) - 1);
-    lane_at[0][i] = (uint32_t(SMALL ? 0 : r) * c.ku.token + unit) << 4;
-    lane_at[1][i] = (uint32_t(SMALL ? 0 : r) * c.vu.token + unit) << 4;
-  }
-  uint32_t lanes = ~0u;
-  auto request = [&](int base, const void* p0, const UnitStrides& u, const uint32_t (&at_lane)[kLoads],
-                     const uint8_t* scale, uint4 (&in)[2][kLoads], uint32_t (&in_scale)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = uint32_t(page[h]) < uint32_t(c.num_pages) ? page[h] : 0;
-      const int slot = (base + 16 * h + (SMALL ? r : 0)) & in_page;
-      const char* q = static_cast<const char*>(p0) + row_at(u, at, slot, kvh);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) in[h][i] = load_from(q, at_lane[i] & lanes);
-      if (FP8) in_scale[h] = scale[((int64_t(at) * c.heads + kvh) << c.page_shift) + slot + (SMALL ? 0 : r)];
-    }
-  };
-  auto request_keys = [&](int base) { request(base, c.k, c.ku, lane_at[0], c.k_scale, kr, ks); };
-  auto request_values = [&](int base) {
-    request(base, c.v, c.vu, lane_at[1], c.v_scale, vr, vs);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      have[h] = uint32_t(page[h]) < uint32_t(c.num_pages) && base + 16 * h + r < end;
-  };
-
-  const int stride = kAttnWaves * kBlock;
-  int base = begin + wave * kBlock;
-  uint16_t* const mine = values[wave];
-  if (base < end) {
-  pages(base);
-  request_keys(base);
-  request_values(base);
-  pages(base + stride < end ? base + stride : base);
-  do {
-    // S^T, a block's 16 tokens by 16 rows at a time
-    f32x4 s[2][MT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) s[h][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 kf;
-        if (FP8) {
-          const uint4 w = kr[h][st >> 1];
-          kf = dequant8((st & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), scale_of(ks[h]));
-        } else {
-          kf = kr[h][st];
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) s[h][m] = mfma16(kf, qf[m][st], s[h][m]);
-      }
-    // Behind the wave's last block every lane asks for one word of the same
-    // block again, which nothing reads: loads on one path only would have to be
-    // waited for as if on the other.
-    const bool more = base + stride < end;
-    const int next = more ? base + stride : base;
-    lanes = more ? ~0u : 0u;
-    request_keys(next);
-    // every row sees every token of the block, unless it reaches beyond the
-    // first row's place or the last row's window, or lacks tokens
-    const bool whole = __all(have[0] && have[1]) && base + kBlock - 1 <= first_place &&
-                       (a.window == 0 || base > last_place - a.window);
-    uint32_t hidden = 0, nan = 0;  // bit 16 h + i: token 16 h + i is absent; its value is not finite
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint16_t* const to = mine + (16 * h + r) * kPitch<DP> + (FP8 ? 16 : 8) * g;
-      uint32_t bad = 0;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        if (FP8) {
-          const float vscale = scale_of(vs[h]);
-          const uint4 lo = dequant8(make_uint2(vr[h][i].x, vr[h][i].y), vscale);
-          const uint4 hi = dequant8(make_uint2(vr[h][i].z, vr[h][i].w), vscale);
-          *reinterpret_cast<uint4*>(to + 64 * i) = lo;
-          *reinterpret_cast<uint4*>(to + 64 * i + 8) = hi;
-          if (!whole) bad |= not_finite8(lo) | not_finite8(hi);
-        } else {
-          *reinterpret_cast<uint4*>(to + 32 * i) = vr[h][i];
-          if (!whole) bad |= not_finite8(vr[h][i]);
-        }
-      }
-      if (!whole) {
-        // a weight of zero does not stop a value that is not finite: such
-        // values are taken out, and their tokens' scores made NaN instead
-        uint64_t any = __ballot(bad != 0 && have[h]);
-        any |= any >> 32;
-        any |= any >> 16;
-        nan |= uint32_t(any & 0xffffu) << (16 * h);
-        hidden |= uint32_t(~__ballot(have[h]) & 0xffffu) << (16 * h);
-        asm volatile("" ::: "memory");  // (a store of its own: else every value would be chosen in registers first)
-        if (!have[h] || ((any >> r) & 1u)) {
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
-            *reinterpret_cast<uint4*>(to + (FP8 ? 64 : 32) * i) = make_uint4(0u, 0u, 0u, 0u);
-            if (FP8) *reinterpret_cast<uint4*>(to + 64 * i + 8) = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-      }
-    }
-    request_values(next);
-    pages(next + stride < end ? next + stride : next);
-    if (!whole) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 16 * h + 4 * g + i, j = base + k;
-          const bool off = (hidden >> k) & 1u, bad = (nan >> k) & 1u;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const bool sees = !off & (j <= place[m]) & (j > oldest[m]);
-            const float x = bad ? NAN : s[h][m][i];
-            s[h][m][i] = sees ? x : -INFINITY;
-          }
-        }
-    }
-    // values are read from LDS four channel tiles ahead of their products
-    uint4 vf[2][4];
-    const uint16_t* const vt = mine + (4 * g + (r >> 2)) * kPitch<DP> + 4 * (r & 3);
-    auto read_values = [&](int d) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint2 v0 = read_transposed(vt + 16 * (d + i));
-        const uint2 v1 = read_transposed(vt + 16 * kPitch<DP> + 16 * (d + i));
-        vf[(d >> 2) & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
-      }
-    };
-    read_values(0);
-    // weights, in place of the scores, and the running statistics
-    uint4 pf[MT];
+    // queries: the B operand, lane (row, g) holding the channels of its steps
+    const int chunks = c.D >> 3;
+    uint4 qf[MT][kSteps];
+    int place[MT], oldest[MT];  // of the lane's rows: they see the tokens oldest < j <= place
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      const int row = 16 * m + r;
+      const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
+      place[m] = row < t.rows ? t.place0 + tok : -1;
+      oldest[m] = a.window > 0 ? max(place[m], -1) - a.window : -1;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int ch = FP8 ? 8 * (s >> 1) + 2 * g + (s & 1) : 4 * s + g;
+        qf[m][s] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < t.rows && ch < chunks) qf[m][s] = *reinterpret_cast<const uint4*>(q + 8 * ch);
+      }
+    }
+    const int first_place = t.place0 + t.first_row / G;  // the places of the tile's first and last rows
+    const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
+    const float sc = a.scale * kLog2e;
+
+    f32x4 o[kDT][MT];
+    float mx[MT], l[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mx[m] = -INFINITY;
+      l[m] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    uint4 kr[2][kLoads], vr[2][kLoads];
+    uint32_t ks[2] = {127, 127}, vs[2] = {127, 127};
+    bool have[2];
+    const int64_t table = b * c.table_stride;
+    const int in_page = (1 << c.page_shift) - 1;
+    // the page table's entries of the block's tokens 0 .. 15 and 16 .. 31 (SMALL:
+    // of this lane's, r and 16 + r), or of the last token in their place
+    int page[2];
+    auto pages = [&](int base) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = min(base + 16 * h + (SMALL ? r : 0), end - 1);
+        page[h] = SMALL ? c.table[table + (j >> c.page_shift)] : uniform_at(c.table, table + (j >> c.page_shift));
+      }
+    };
+    // ask for a block's rows; the loads of absent tokens and of channels beyond
+    // the head's go to page 0 and to its last channels, and are not used
+    uint32_t lane_at[2][kLoads];  // bytes from the 16 tokens' first row, of keys and of values
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t unit = min(4 * i + g, (FP8 ? c.D >> 4 : c.D >> 3) - 1);
+      lane_at[0][i] = (uint32_t(SMALL ? 0 : r) * c.ku.token + unit) << 4;
+      lane_at[1][i] = (uint32_t(SMALL ? 0 : r) * c.vu.token + unit) << 4;
+    }
+    uint32_t lanes = ~0u;
+    auto request = [&](int base, const void* p0, const UnitStrides& u, const uint32_t (&at_lane)[kLoads],
+                       const uint8_t* scale, uint4 (&in)[2][kLoads], uint32_t (&in_scale)[2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = uint32_t(page[h]) < uint32_t(c.num_pages) ? page[h] : 0;
+        const int slot = (base + 16 * h + (SMALL ? r : 0)) & in_page;
+        const char* q = static_cast<const char*>(p0) + row_at(u, at, slot, kvh);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) in[h][i] = load_from(q, at_lane[i] & lanes);
+        if (FP8) in_scale[h] = scale[((int64_t(at) * c.heads + kvh) << c.page_shift) + slot + (SMALL ? 0 : r)];
+      }
+    };
+    auto request_keys = [&](int base) { request(base, c.k, c.ku, lane_at[0], c.k_scale, kr, ks); };
+    auto request_values = [&](int base) {
+      request(base, c.v, c.vu, lane_at[1], c.v_scale, vr, vs);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        have[h] = uint32_t(page[h]) < uint32_t(c.num_pages) && base + 16 * h + r < end;
+    };
+
+    const int stride = kAttnWaves * kBlock;
+    int base = begin + wave * kBlock;
+    uint16_t* const mine = values[wave];
+    if (base < end) {
+      pages(base);
+      request_keys(base);
+      request_values(base);
+      pages(base + stride < end ? base + stride : base);
+      do {
+        // S^T, a block's 16 tokens by 16 rows at a time
+        f32x4 s[2][MT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) s[h][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 kf;
+            if (FP8) {
+              const uint4 w = kr[h][st >> 1];
+              kf = dequant8((st & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), scale_of(ks[h]));
+            } else {
+              kf = kr[h][st];
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s[h][m] = mfma16(kf, qf[m][st], s[h][m]);
+          }
+        // Behind the wave's last block every lane asks for one word of the same
+        // block again, which nothing reads: loads on one path only would have to be
+        // waited for as if on the other.
+        const bool more = base + stride < end;
+        const int next = more ? base + stride : base;
+        lanes = more ? ~0u : 0u;
+        request_keys(next);
+        // every row sees every token of the block, unless it reaches beyond the
+        // first row's place or the last row's window, or lacks tokens
+        const bool whole = __all(have[0] && have[1]) && base + kBlock - 1 <= first_place &&
+                           (a.window == 0 || base > last_place - a.window);
+        uint32_t hidden = 0, nan = 0;  // bit 16 h + i: token 16 h + i is absent; its value is not finite
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint16_t* const to = mine + (16 * h + r) * kPitch<DP> + (FP8 ? 16 : 8) * g;
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            if (FP8) {
+              const float vscale = scale_of(vs[h]);
+              const uint4 lo = dequant8(make_uint2(vr[h][i].x, vr[h][i].y), vscale);
+              const uint4 hi = dequant8(make_uint2(vr[h][i].z, vr[h][i].w), vscale);
+              *reinterpret_cast<uint4*>(to + 64 * i) = lo;
+              *reinterpret_cast<uint4*>(to + 64 * i + 8) = hi;
+              if (!whole) bad |= not_finite8(lo) | not_finite8(hi);
+            } else {
+              *reinterpret_cast<uint4*>(to + 32 * i) = vr[h][i];
+              if (!whole) bad |= not_finite8(vr[h][i]);
+            }
+          }
+          if (!whole) {
+            // a weight of zero does not stop a value that is not finite: such
+            // values are taken out, and their tokens' scores made NaN instead
+            uint64_t any = __ballot(bad != 0 && have[h]);
+            any |= any >> 32;
+            any |= any >> 16;
+            nan |= uint32_t(any & 0xffffu) << (16 * h);
+            hidden |= uint32_t(~__ballot(have[h]) & 0xffffu) << (16 * h);
+            asm volatile("" ::: "memory");  // (a store of its own: else every value would be chosen in registers first)
+            if (!have[h] || ((any >> r) & 1u)) {
+#pragma unroll
+              for (int i = 0; i < kLoads; ++i) {
+                *reinterpret_cast<uint4*>(to + (FP8 ? 64 : 32) * i) = make_uint4(0u, 0u, 0u, 0u);
+                if (FP8) *reinterpret_cast<uint4*>(to + 64 * i + 8) = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+          }
+        }
+        request_values(next);
+        pages(next + stride < end ? next + stride : next);
+        if (!whole) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 16 * h + 4 * g + i, j = base + k;
+              const bool off = (hidden >> k) & 1u, bad = (nan >> k) & 1u;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                const bool sees = !off & (j <= place[m]) & (j > oldest[m]);
+                const float x = bad ? NAN : s[h][m][i];
+                s[h][m][i] = sees ? x : -INFINITY;
+              }
+            }
+        }
+        // values are read from LDS four channel tiles ahead of their products
+        uint4 vf[2][4];
+        const uint16_t* const vt = mine + (4 * g + (r >> 2)) * kPitch<DP> + 4 * (r & 3);
+        auto read_values = [&](int d) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 v0 = read_transposed(vt + 16 * (d + i));
+            const uint2 v1 = read_transposed(vt + 16 * kPitch<DP> + 16 * (d + i));
+            vf[(d >> 2) & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+          }
+        };
+        read_values(0);
+        // weights, in place of the scores, and the running statistics
+        uint4 pf[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[h][m][i]);
+          top = max_over_quarters(top);
+          const bool ahead = (top - mx[m]) * sc > kSlack;
+          if (__any(ahead)) {
+            const float higher = ahead ? top : mx[m];  // (one row's scores change no other row's roundings)
+            const float keep = fast_exp2((mx[m] - (higher == -INFINITY ? 0.f : higher)) * sc);
+            mx[m] = higher;
+            l[m] *= keep;
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
+          }
+          const float ref = mx[m] == -INFINITY ? 0.f : mx[m] * sc;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[h][m][i] = fast_exp2(fmaf(s[h][m][i], sc, -ref));
+              l[m] += s[h][m][i];
+            }
+          // rounded to bf16 for the product: a weight is off by at most 2^-8 of itself
+          pf[m] = make_uint4(pack_bf16(s[0][m][0], s[0][m][1]), pack_bf16(s[0][m][2], s[0][m][3]),
+                             pack_bf16(s[1][m][0], s[1][m][1]), pack_bf16(s[1][m][2], s[1][m][3]));
+        }
+#pragma unroll
+        for (int d = 0; d < kDT; d += 4) {
+          if (d + 4 < kDT) read_values(d + 4);
+          keep_order();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) o[d + i][m] = mfma16(vf[(d >> 2) & 1][i], pf[m], o[d + i][m]);
+          keep_order();
+        }
+        base += stride;
+      } while (base < end);
+    }
+
+    // join the waves: the tile's maximum, then each wave's results scaled to it
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      l[m] += __shfl_xor(l[m], 16, 64);
+      l[m] += __shfl_xor(l[m], 32, 64);
+      if (g == 0) {
+        stat_m[wave][16 * m + r] = mx[m];
+        stat_l[wave][16 * m + r] = l[m];
+      }
+    }
+    __syncthreads();
+    const bool alone = live.first == live.last;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // (what follows from it is formed here, not kept in registers through the loop)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (16 * m >= t.rows) break;
+      const int row = 16 * m + r;
       float top = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][row]);
+      const float ref = top == -INFINITY ? 0.f : top * sc;
+      const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
+      // rows of DP channels and 16 bytes more, which keep 8 rows' stores apart
+      float* part = reinterpret_cast<float*>(values[wave]) + r * (DP + 4) + 4 * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[h][m][i]);
-      top = max_over_quarters(top);
-      const bool ahead = (top - mx[m]) * sc > kSlack;
-      if (__any(ahead)) {
-        const float higher = ahead ? top : mx[m];  // (one row's scores change no other row's roundings)
-        const float keep = fast_exp2((mx[m] - (higher == -INFINITY ? 0.f : higher)) * sc);
-        mx[m] = higher;
-        l[m] *= keep;
+      for (int d = 0; d < kDT; ++d)
+        *reinterpret_cast<float4*>(part + 16 * d) =
+            make_float4(o[d][m][0] * keep, o[d][m][1] * keep, o[d][m][2] * keep, o[d][m][3] * keep);
+      __syncthreads();
+      // 16 rows by 16 threads, 8 channels at a time
+      const int orow = tid >> 4;
+      const int trow = 16 * m + orow;
+      if (trow < t.rows) {
+        float rtop = -INFINITY, total = 0.f;
 #pragma unroll
-        for (int d = 0; d < kDT; ++d) o[d][m] *= keep;
-      }
-      const float ref = mx[m] == -INFINITY ? 0.f : mx[m] * sc;
+        for (int w = 0; w < kAttnWaves; ++w) rtop = fmaxf(rtop, stat_m[w][trow]);
+        const float rref = rtop == -INFINITY ? 0.f : rtop * sc;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int w = 0; w < kAttnWaves; ++w) total += stat_l[w][trow] * fast_exp2(fmaf(stat_m[w][trow], sc, -rref));
+        const int tok = t.token0 + (t.first_row + trow) / G, head = kvh * G + (t.first_row + trow) % G;
+        const int64_t at = int64_t(tok) * a.q_heads + head;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        for (int ch = tid & 15; ch < chunks; ch += 16) {
+          float y[8] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[h][m][i] = fast_exp2(fmaf(s[h][m][i], sc, -ref));
-          l[m] += s[h][m][i];
+          for (int w = 0; w < kAttnWaves; ++w) {
+            float x[8];
+            load8(reinterpret_cast<const float*>(values[w]) + orow * (DP + 4) + 8 * ch, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += x[j];
+          }
+          if (alone) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= inv;
+          }
+          if (alone)
+            store8(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + 8 * ch, y);
+          else
+            store8(p.part_o + (split * (int64_t(a.T) * a.q_heads) + at) * c.D + 8 * ch, y);
         }
-      // rounded to bf16 for the product: a weight is off by at most 2^-8 of itself
-      pf[m] = make_uint4(pack_bf16(s[0][m][0], s[0][m][1]), pack_bf16(s[0][m][2], s[0][m][3]),
-                         pack_bf16(s[1][m][0], s[1][m][1]), pack_bf16(s[1][m][2], s[1][m][3]));
-    }
-#pragma unroll
-    for (int d = 0; d < kDT; d += 4) {
-      if (d + 4 < kDT) read_values(d + 4);
-      keep_order();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) o[d + i][m] = mfma16(vf[(d >> 2) & 1][i], pf[m], o[d + i][m]);
-      keep_order();
-    }
-    base += stride;
-  } while (base < end);
-  }
-
-  // join the waves: the tile's maximum, then each wave's results scaled to it
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    l[m] += __shfl_xor(l[m], 16, 64);
-    l[m] += __shfl_xor(l[m], 32, 64);
-    if (g == 0) {
-      stat_m[wave][16 * m + r] = mx[m];
-      stat_l[wave][16 * m + r] = l[m];
-    }
-  }
-  __syncthreads();
-  const bool alone = live.first == live.last;
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));  // (what follows from it is formed here, not kept in registers through the loop)
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (16 * m >= t.rows) break;
-    const int row = 16 * m + r;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, stat_m[w][row]);
-    const float ref = top == -INFINITY ? 0.f : top * sc;
-    const float keep = fast_exp2(fmaf(mx[m], sc, -ref));
-    // rows of DP channels and 16 bytes more, which keep 8 rows' stores apart
-    float* part = reinterpret_cast<float*>(values[wave]) + r * (DP + 4) + 4 * g;
-#pragma unroll
-    for (int d = 0; d < kDT; ++d)
-      *reinterpret_cast<float4*>(part + 16 * d) =
-          make_float4(o[d][m][0] * keep, o[d][m][1] * keep, o[d][m][2] * keep, o[d][m][3] * keep);
-    __syncthreads();
-    // 16 rows by 16 threads, 8 channels at a time
-    const int orow = tid >> 4;
-    const int trow = 16 * m + orow;
-    if (trow < t.rows) {
-      float rtop = -INFINITY, total = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) rtop = fmaxf(rtop, stat_m[w][trow]);
-      const float rref = rtop == -INFINITY ? 0.f : rtop * sc;
-#pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) total += stat_l[w][trow] * fast_exp2(fmaf(stat_m[w][trow], sc, -rref));
-      const int tok = t.token0 + (t.first_row + trow) / G, head = kvh * G + (t.first_row + trow) % G;
-      const int64_t at = int64_t(tok) * a.q_heads + head;
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-      for (int ch = tid & 15; ch < chunks; ch += 16) {
-        float y[8] = {};
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
-          float x[8];
-          load8(reinterpret_cast<const float*>(values[w]) + orow * (DP + 4) + 8 * ch, x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] += x[j];
+        if ((tid & 15) == 0) {
+          if (!alone)
+            p.part_ml[split * (int64_t(a.T) * a.q_heads) + at] = make_float2(rtop == -INFINITY ? rtop : rref, total);
+          else if (a.lse)
+            a.lse[at] = total == 0.f ? -INFINITY : (rref + fast_log2(total)) * kLn2;
         }
-        if (alone) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] *= inv;
-        }
-        if (alone)
-          store8(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + 8 * ch, y);
-        else
-          store8(p.part_o + (split * (int64_t(a.T) * a.q_heads) + at) * c.D + 8 * ch, y);
       }
-      if ((tid & 15) == 0) {
-        if (!alone)
-          p.part_ml[split * (int64_t(a.T) * a.q_heads) + at] = make_float2(rtop == -INFINITY ? rtop : rref, total);
-        else if (a.lse)
-          a.lse[at] = total == 0.f ? -INFINITY : (rref + fast_log2(total)) * kLn2;
-      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
   }
 }
 
@@ -515,7 +540,8 @@ constexpr int kManyRows = 32 * kAttnWaves;
 // offset), every thread looks its tokens' pages up; 1 a load's tokens of a wave
 // lie in one page; 2 the tile lies in one page.
 template <int DP, bool FP8, int PAGES>
-__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void many_rows_kernel(AttnArgs a, AttnPlan p) {
+__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void many_rows_kernel(
+    AttnArgs a, AttnPlan p) {
   constexpr int M = kManyRows;
   constexpr int kSteps = DP / 16;
   constexpr int kDT = DP / 32;
@@ -713,109 +739,109 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       request(next, c.k, c.ku, c.k_scale, kin, kscale);
       request(next, c.v, c.vu, c.v_scale, vin, vscale);
       if (busy) {  // (a wave without rows only helps to load)
-      f32x16 s[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
-      // products in groups whose operands are read a group ahead; a wave
-      // that has products to issue goes before one in its softmax (349 -> 343 us)
-      {
-        const uint16_t* const kt = &keys[buf][r * kPitch<DP> + 8 * h];
-        uint4 kf[2][kGroup];
-        auto read = [&](int n) {
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i)
-            kf[n / kGroup & 1][i] =
-                *reinterpret_cast<const uint4*>(kt + 32 * ((n + i) & 1) * kPitch<DP> + 16 * ((n + i) >> 1));
-        };
-        read(0);
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int n = 0; n < 2 * kSteps; n += kGroup) {
-          if (n + kGroup < 2 * kSteps) read(n + kGroup);
-          keep_order();
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i)
-            s[(n + i) & 1] = mfma32(kf[n / kGroup & 1][i], qf[(n + i) >> 1], s[(n + i) & 1]);
-          keep_order();
-        }
-      }
-      __builtin_amdgcn_s_setprio(0);
-      const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
-      if (!whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0) {
+        f32x16 s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(&state[buf][32 * u + 8 * k + 4 * h]);
+          for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+        // products in groups whose operands are read a group ahead; a wave
+        // that has products to issue goes before one in its softmax (343 -> 334 us)
+        {
+          const uint16_t* const kt = &keys[buf][r * kPitch<DP> + 8 * h];
+          uint4 kf[2][kGroup];
+          auto read = [&](int n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = base + 32 * u + 8 * k + 4 * h + i;
-              const uint32_t is = (w >> (8 * i)) & 0xffu;
-              const bool sees = (is != 1) & (j <= place) & (j > oldest);
-              const float x = is == 2 ? NAN : s[u][4 * k + i];
-              s[u][4 * k + i] = sees ? x : -INFINITY;
-            }
+            for (int i = 0; i < kGroup; ++i)
+              kf[n / kGroup & 1][i] =
+                  *reinterpret_cast<const uint4*>(kt + 32 * ((n + i) & 1) * kPitch<DP> + 16 * ((n + i) >> 1));
+          };
+          read(0);
+          __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+          for (int n = 0; n < 2 * kSteps; n += kGroup) {
+            if (n + kGroup < 2 * kSteps) read(n + kGroup);
+            keep_order();
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+              s[(n + i) & 1] = mfma32(kf[n / kGroup & 1][i], qf[(n + i) >> 1], s[(n + i) & 1]);
+            keep_order();
           }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-      top = max_over_halves(top);
-      const bool ahead = (top - mx) * sc > kSlack;
-      if (__any(ahead)) {
-        const float higher = ahead ? top : mx;  // (one row's scores change no other row's roundings)
-        const float keep = fast_exp2((mx - (higher == -INFINITY ? 0.f : higher)) * sc);
-        mx = higher;
-        l *= keep;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) o[d] *= keep;
-      }
-      const float ref = mx == -INFINITY ? 0.f : mx * sc;
-      const uint16_t* const vt =
-          &values[buf][(4 * h + ((lane & 15) >> 2)) * kValuePitch<DP> + (lane & 16) + 4 * (lane & 3)];
-      uint4 vf[2][kGroup];
-      auto read_values = [&](int n) {
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          const int at = n + i, d = at % kDT, t16 = at / kDT;  // channels 32 d .., tokens 16 t16 ..
-          const uint2 v0 = read_transposed(vt + 16 * t16 * kValuePitch<DP> + 32 * d);
-          const uint2 v1 = read_transposed(vt + (16 * t16 + 8) * kValuePitch<DP> + 32 * d);
-          vf[n / kGroup & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
         }
-      };
-      read_values(0);
-      uint4 pf[2][2];
+        __builtin_amdgcn_s_setprio(0);
+        const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
+        if (!whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[u][i] = fast_exp2(fmaf(s[u][i], sc, -ref));
-          l += s[u][i];
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(&state[buf][32 * u + 8 * k + 4 * h]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = base + 32 * u + 8 * k + 4 * h + i;
+                const uint32_t is = (w >> (8 * i)) & 0xffu;
+                const bool sees = (is != 1) & (j <= place) & (j > oldest);
+                const float x = is == 2 ? NAN : s[u][4 * k + i];
+                s[u][4 * k + i] = sees ? x : -INFINITY;
+              }
+            }
         }
-        // rounded to bf16 for the product: a weight is off by at most 2^-8 of itself
+        float top = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          pf[u][q] = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
-                                pack_bf16(s[u][8 * q + 4], s[u][8 * q + 5]),
-                                pack_bf16(s[u][8 * q + 6], s[u][8 * q + 7]));
-      }
-      __builtin_amdgcn_s_setprio(1);
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int n = 0; n < 4 * kDT; n += kGroup) {
-        if (n + kGroup < 4 * kDT) read_values(n + kGroup);
-        keep_order();
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top = max_over_halves(top);
+        const bool ahead = (top - mx) * sc > kSlack;
+        if (__any(ahead)) {
+          const float higher = ahead ? top : mx;  // (one row's scores change no other row's roundings)
+          const float keep = fast_exp2((mx - (higher == -INFINITY ? 0.f : higher)) * sc);
+          mx = higher;
+          l *= keep;
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          const int at = n + i, d = at % kDT, t16 = at / kDT;
-          o[d] = mfma32(vf[n / kGroup & 1][i], pf[t16 >> 1][t16 & 1], o[d]);
+          for (int d = 0; d < kDT; ++d) o[d] *= keep;
         }
-        keep_order();
-      }
-      __builtin_amdgcn_s_setprio(0);
+        const float ref = mx == -INFINITY ? 0.f : mx * sc;
+        const uint16_t* const vt =
+            &values[buf][(4 * h + ((lane & 15) >> 2)) * kValuePitch<DP> + (lane & 16) + 4 * (lane & 3)];
+        uint4 vf[2][kGroup];
+        auto read_values = [&](int n) {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            const int at = n + i, d = at % kDT, t16 = at / kDT;  // channels 32 d .., tokens 16 t16 ..
+            const uint2 v0 = read_transposed(vt + 16 * t16 * kValuePitch<DP> + 32 * d);
+            const uint2 v1 = read_transposed(vt + (16 * t16 + 8) * kValuePitch<DP> + 32 * d);
+            vf[n / kGroup & 1][i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+          }
+        };
+        read_values(0);
+        uint4 pf[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[u][i] = fast_exp2(fmaf(s[u][i], sc, -ref));
+            l += s[u][i];
+          }
+          // rounded to bf16 for the product: a weight is off by at most 2^-8 of itself
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            pf[u][q] = make_uint4(pack_bf16(s[u][8 * q], s[u][8 * q + 1]), pack_bf16(s[u][8 * q + 2], s[u][8 * q + 3]),
+                                  pack_bf16(s[u][8 * q + 4], s[u][8 * q + 5]),
+                                  pack_bf16(s[u][8 * q + 6], s[u][8 * q + 7]));
+        }
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int n = 0; n < 4 * kDT; n += kGroup) {
+          if (n + kGroup < 4 * kDT) read_values(n + kGroup);
+          keep_order();
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            const int at = n + i, d = at % kDT, t16 = at / kDT;
+            o[d] = mfma32(vf[n / kGroup & 1][i], pf[t16 >> 1][t16 & 1], o[d]);
+          }
+          keep_order();
+        }
+        __builtin_amdgcn_s_setprio(0);
       }
       stage_keys(buf ^ 1);
       stage_values(next, buf ^ 1);
@@ -867,6 +893,8 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
 // One workgroup per row and head.  Every wave forms the row's maximum and sum
 // from the splits' (a lane each); then groups of 32 (64 above 128 channels)
 // lanes take the splits in turn, four channels a lane, and are added in LDS.
+// Bound by latency (a launch, the lengths, the parts, an LDS exchange): 8 us for
+// 2048 rows of 4 splits, 9 us for 1152 of 32, 4 us for a single token's.
 template <int M>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan p) {
   __shared__ float4 part[kAttnThreads];
@@ -996,8 +1024,8 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   // enough workgroups to fill the compute units twice over, of at least 256
   // tokens each; eight times with one tile of rows, whose parts cost little, so
   // that requests of different lengths even out (1024 to 4096 tokens in a batch
-  // of 64: 151 us filled twice, 142 us eight times; with 5 rows a head of 4096
-  // 8-bit tokens each, 119 and 143 us)
+  // of 64: 150 us filled twice, 141 us eight times; but 5 new tokens of 4 heads
+  // over 4096 8-bit ones, 119 and 143 us)
   const int64_t groups = int64_t(B) * p.tiles * kv_heads;
   const int64_t want = p.row_tile == 16 ? 2048 : 512;
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
