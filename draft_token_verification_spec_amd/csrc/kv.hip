@@ -5,8 +5,8 @@
 // rows, and then all threads move 8 channels at a time, a thread keeping its
 // head and channels over the rows so that its loads do not wait for one
 // another.  Measured: 87 thousand rows of 8 heads of 128 8-bit channels as bf16,
-// 187 MB read and 357 MB written in 112 to 121 us (4.5 to 4.9 TB/s; a plain copy
-// reaches 5.1); 1125 bf16 rows of 8 heads of 64 in 4.4 us (latency: a launch,
+// 180 MB read and 357 MB written in 112 to 121 us (4.5 to 4.9 TB/s; a plain copy
+// reaches 5.1); 1123 bf16 rows of 8 heads of 64 in 4.4 us (latency: a launch,
 // the search, the page, the row).
 #include "sv_attn.hpp"
 
