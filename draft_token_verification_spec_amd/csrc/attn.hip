@@ -554,7 +554,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
   __shared__ __align__(16) uint16_t keys[2][kTile * kPitch<DP>];
   __shared__ __align__(16) uint16_t values[2][kTile * kValuePitch<DP>];
   __shared__ __align__(16) uint8_t state[2][kTile];   // of a token: 0 present, 1 absent, 2 a value not finite
-  __shared__ __align__(16) int lacks[2][kAttnWaves];  // some token that this wave loaded is absent
+  __shared__ __align__(16) int marks[2][kAttnWaves];  // some token that this wave loaded has a state
 
   const CacheView& c = a.cache;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -598,8 +598,14 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
     const int oldest = a.window > 0 ? max(place, -1) - a.window : -1;  // the row sees the tokens oldest < j <= place
     const int first_place = t.place0 + t.first_row / G;
     const int last_place = t.place0 + (t.first_row + t.rows - 1) / G;
+    const int last_oldest = a.window > 0 ? max(last_place, -1) - a.window : -1;
     const float sc = a.scale * kLog2e;
     const bool busy = 32 * wave < t.rows;
+    // the places of the wave's first and last rows, and the last tokens before their windows
+    const int wave_first = uniform(t.place0 + (t.first_row + 32 * wave) / G);
+    const int wave_last = uniform(t.place0 + (t.first_row + min(32 * wave + 31, t.rows - 1)) / G);
+    const int wave_oldest = a.window > 0 ? max(wave_first, -1) - a.window : -1;
+    const int wave_newest = a.window > 0 ? max(wave_last, -1) - a.window : -1;
 
     f32x16 o[kDT];
 #pragma unroll
@@ -653,7 +659,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
     };
     // every row of the tile sees all 64 tokens, as far as places go
     auto whole = [&](int base) {
-      return base + kTile - 1 <= first_place && base + kTile <= end && (a.window == 0 || base > last_place - a.window);
+      return base + kTile - 1 <= first_place && base + kTile <= end && base > last_oldest;
     };
     auto stage_keys = [&](int buf) {
       uint16_t* const to = &keys[buf][tid / kLanes * kPitch<DP> + 8 * kParts * (tid % kLanes)];
@@ -668,7 +674,7 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
         }
       }
     };
-    int marked = 0;  // bit buf: this wave has left marks in state[buf] and lacks[buf]
+    int marked = 0;  // bit buf: this wave has left marks in state[buf] and marks[buf]
     auto stage_values = [&](int base, int buf) {
       const bool ok = whole(base);
       uint16_t* const to = &values[buf][tid / kLanes * kValuePitch<DP> + 8 * kParts * (tid % kLanes)];
@@ -710,16 +716,16 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
             *reinterpret_cast<uint4*>(to + kSpan * i * kValuePitch<DP> + 8 * q) = make_uint4(0u, 0u, 0u, 0u);
         }
         if (tid % kLanes == 0) state[buf][at] = gone ? 1 : spoiled ? 2 : 0;
-        some |= gone;
+        some |= gone || spoiled;
       }
       some = __any(some);
-      if (lane == 0) lacks[buf][wave] = some;
+      if (lane == 0) marks[buf][wave] = some;
       marked = trouble ? marked | (1 << buf) : marked & ~(1 << buf);
     };
 
     // (the barrier that ended the loop has ended every read of a former tile)
     if (tid < kTile) state[0][tid] = state[1][tid] = 0;
-    if (tid < kAttnWaves) lacks[0][tid] = lacks[1][tid] = 0;
+    if (tid < kAttnWaves) marks[0][tid] = marks[1][tid] = 0;
     __syncthreads();
     int buf = 0;
     if (begin < end) {
@@ -738,7 +744,8 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
       const int next = base + kTile;
       request(next, c.k, c.ku, c.k_scale, kin, kscale);
       request(next, c.v, c.vu, c.v_scale, vin, vscale);
-      if (busy) {  // (a wave without rows only helps to load)
+      // a wave without rows, or whose rows do not reach this far, only helps to load
+      if (busy && base <= wave_last && base + kTile - 1 > wave_oldest) {
         f32x16 s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -768,8 +775,9 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
           }
         }
         __builtin_amdgcn_s_setprio(0);
-        const int4 lack = *reinterpret_cast<const int4*>(lacks[buf]);
-        if (!whole(base) || (lack.x | lack.y | lack.z | lack.w) != 0) {
+        // scores of absent tokens, of values taken out, and of tokens that the row does not see
+        const int4 mark = *reinterpret_cast<const int4*>(marks[buf]);
+        if ((mark.x | mark.y | mark.z | mark.w) != 0) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -777,13 +785,26 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
               const uint32_t w = *reinterpret_cast<const uint32_t*>(&state[buf][32 * u + 8 * k + 4 * h]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int j = base + 32 * u + 8 * k + 4 * h + i;
                 const uint32_t is = (w >> (8 * i)) & 0xffu;
-                const bool sees = (is != 1) & (j <= place) & (j > oldest);
-                const float x = is == 2 ? NAN : s[u][4 * k + i];
-                s[u][4 * k + i] = sees ? x : -INFINITY;
+                if (is != 0) s[u][4 * k + i] = is == 1 ? -INFINITY : NAN;
               }
             }
+        }
+        if (base + kTile - 1 > wave_first) {
+          const int upto = place - base - 4 * h;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (32 * u + 8 * (i >> 2) + (i & 3) > upto) s[u][i] = -INFINITY;
+        }
+        if (base <= wave_newest) {
+          const int past = oldest - base - 4 * h;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (32 * u + 8 * (i >> 2) + (i & 3) <= past) s[u][i] = -INFINITY;
         }
         float top = -INFINITY;
 #pragma unroll
