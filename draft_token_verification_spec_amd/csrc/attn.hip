@@ -1041,13 +1041,14 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   const int64_t most_tiles = (1 << 20) / (B > 0 ? B : 1);  // (tiles of all requests and heads: 32 bits)
   tiles = tiles < most_tiles ? tiles : most_tiles;
   p.tiles = int(tiles < 1 ? 1 : tiles);
-  // enough workgroups to fill the compute units twice over, of at least 256
-  // tokens each; eight times with one tile of rows, whose parts cost little, so
-  // that requests of different lengths even out (1024 to 4096 tokens in a batch
-  // of 64: 150 us filled twice, 141 us eight times; but 5 new tokens of 4 heads
-  // over 4096 8-bit ones, 119 and 143 us)
+  // Enough workgroups to fill the compute units twice over, of at least 256
+  // tokens each; four times with two tiles of rows and eight times with one,
+  // whose parts cost little, so that requests of different lengths even out (one:
+  // 1024 to 4096 tokens in a batch of 64, 150 us filled twice, 138 us eight times;
+  // two: 5 new tokens of 4 heads behind 100 to 8000, 16 requests 78 us filled
+  // twice, 68 four times, 63 eight times, but equal lengths of 4096 61, 60 and 67).
   const int64_t groups = int64_t(B) * p.tiles * kv_heads;
-  const int64_t want = p.row_tile == 16 ? 2048 : 512;
+  const int64_t want = p.row_tile == 16 ? 2048 : p.row_tile == 32 ? 1024 : 512;
   int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
   n = n < (max_kv_len + 255) / 256 ? n : (max_kv_len + 255) / 256;
   // With few of them one compute unit's reads are what counts (about 37 bytes a
