@@ -102,25 +102,32 @@ struct Tile {
   int begin, end;  // tokens that some row of the tile may see
 };
 
-// The tile of request b whose first row is first_row; rows == 0 beyond the
-// request's last.
+// The tile of a request of n rows from token0 on and len cached tokens whose
+// first row is first_row; rows == 0 beyond the request's last.
 template <int M>
-__device__ __forceinline__ Tile tile_at(const AttnArgs& a, int G, int b, int64_t first_row) {
+__device__ __forceinline__ Tile tile_of(const AttnArgs& a, int G, int token0, int64_t n, int64_t len,
+                                        int64_t first_row) {
   Tile t;
   t.rows = 0;
-  t.token0 = uniform_at(a.query_start, b);
-  const int64_t n = int64_t(uniform_at(a.query_start, b + 1)) - t.token0;
+  t.token0 = token0;
   const int64_t rows = n * G - first_row;
   if (t.token0 < 0 || int64_t(t.token0) + n > a.T || rows <= 0) return t;
   t.first_row = int(first_row);
   t.rows = int(min(rows, int64_t(M)));
-  const int64_t len = max(uniform_at(a.kv_len, b), 0);
   const int64_t held = min(len, int64_t(a.cache.max_pages) << a.cache.page_shift);
   const int64_t place0 = len - n;
   t.place0 = int(place0);
   const int64_t first_place = place0 + t.first_row / G, last_place = place0 + (t.first_row + t.rows - 1) / G;
   t.end = int(max(int64_t(0), min(held, last_place + 1)));
   t.begin = a.window > 0 ? int(min(int64_t(t.end), max(int64_t(0), first_place - a.window + 1))) : 0;
+  return t;
+}
+
+// The same of request b, for the whole workgroup.
+template <int M>
+__device__ __forceinline__ Tile tile_at(const AttnArgs& a, int G, int b, int64_t first_row) {
+  const int token0 = uniform_at(a.query_start, b), len = max(uniform_at(a.kv_len, b), 0);
+  Tile t = tile_of<M>(a, G, token0, int64_t(uniform_at(a.query_start, b + 1)) - token0, len, first_row);
   // 64-bit comparisons are vector instructions: back to scalars
   t.token0 = uniform(t.token0), t.rows = uniform(t.rows), t.first_row = uniform(t.first_row);
   t.place0 = uniform(t.place0), t.begin = uniform(t.begin), t.end = uniform(t.end);
@@ -910,86 +917,118 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
 // joining splits
 // ---------------------------------------------------------------------------
 
-// One workgroup per row and head.  Every wave forms the row's maximum and sum
-// from the splits' (a lane each); then groups of 32 (64 above 128 channels)
-// lanes take the splits in turn, four channels a lane, and are added in LDS.
-// Bound by latency (a launch, the lengths, the parts, an LDS exchange): 8 us for
-// 2048 rows of 4 splits, 9 us for 1152 of 32, 4 us for a single token's.
+// A workgroup takes `per` rows (of a token and a head): each lane looks up
+// whether one of them was split, and those that were are joined in turn (a
+// single row is looked up through the scalar cache, 2 us sooner).  Every
+// wave forms the row's maximum and sum from the splits' (a lane each); then groups
+// of 32 (64 above 128 channels) lanes take the splits in turn, four channels a
+// lane, and are added in LDS.
+// Bound by latency (a launch, the lengths, the parts, an LDS exchange): 10 us for
+// 2048 rows of 4 splits and for 1152 of 32, 5 us for a single token's.
 template <int M>
-__global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan p) {
+__global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan p, int per) {
   __shared__ float4 part[kAttnThreads];
   const CacheView& c = a.cache;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int tok = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
-  const int64_t at = blockIdx.x, all = int64_t(a.T) * a.q_heads;
   const int G = a.q_heads / c.heads;
-  // requests of equally many rows are found at once, others by a search
-  int b = int(int64_t(tok) * a.B / a.T);
-  if (tok < uniform_at(a.query_start, b) || tok >= uniform_at(a.query_start, b + 1)) {
-    b = uniform(find_sequence(a.query_start, a.B, tok, lane));
-    if (b < 0 || tok >= uniform_at(a.query_start, b + 1)) return;
-  }
-  // the row's tile, as the kernel that wrote the parts saw it
-  const int64_t row = int64_t(tok - uniform_at(a.query_start, b)) * G + head % G;
-  const Tile t = tile_at<M>(a, G, b, uniform(int(row / M)) * int64_t(M));
-  if (t.rows == 0) return;
-  const Splits live = live_splits(t, p.split_len, p.num_splits);
-  if (live.first == live.last) return;  // written by the split itself
-  // the first parts are asked for along with the statistics
-  constexpr int kAhead = 4;
-  const int lg = c.D <= 128 ? 5 : 6, groups = kAttnThreads >> lg;
-  const int ch = min(4 * (tid & ((1 << lg) - 1)), c.D - 4), mine = live.first + (tid >> lg);
-  auto part_at = [&](int s) {
-    return *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + ch);
+  const int64_t all = int64_t(a.T) * a.q_heads, from = int64_t(blockIdx.x) * per, to = min(from + per, all);
+  // the splits of a row of ours, as the kernel that wrote the parts saw them
+  auto splits_of = [&](int64_t at, auto load) {
+    const int tok = int(at / a.q_heads), head = int(at % a.q_heads);
+    // requests of equally many rows are found at once, others by a search
+    int b = int(int64_t(tok) * a.B / a.T);
+    int token0 = load(a.query_start, b), next = load(a.query_start, b + 1);
+    if (tok < token0 || tok >= next) {
+      int hi = a.B;  // the last request that starts at tok or before is b - 1 in the end
+      for (b = 0; b < hi;) {
+        const int mid = b + ((hi - b) >> 1);
+        if (load(a.query_start, mid) <= tok)
+          b = mid + 1;
+        else
+          hi = mid;
+      }
+      if (--b < 0) return Splits{0, 0};
+      token0 = load(a.query_start, b), next = load(a.query_start, b + 1);
+      if (tok >= next) return Splits{0, 0};
+    }
+    const int64_t row = int64_t(tok - token0) * G + head % G;
+    const Tile t = tile_of<M>(a, G, token0, int64_t(next) - token0, max(load(a.kv_len, b), 0), row / M * M);
+    return t.rows != 0 ? live_splits(t, p.split_len, p.num_splits) : Splits{0, 0};
   };
-  float4 v[kAhead];
-  float m[kAhead];
+  for (int64_t some = from; some < to; some += 64) {
+    Splits mine = {0, 0};
+    if (per == 1)
+      mine = splits_of(blockIdx.x, uniform_at);
+    else if (some + lane < to)
+      mine = splits_of(some + lane, [](const int32_t* x, int64_t i) { return x[i]; });
+    // (a row with one split was written by the split itself)
+    for (uint64_t left = __ballot(mine.first != mine.last && some + lane < to); left != 0; left &= left - 1) {
+      const int k = __builtin_ctzll(left);
+      const Splits live = {__builtin_amdgcn_readlane(mine.first, k), __builtin_amdgcn_readlane(mine.last, k)};
+      const int64_t at = some + k;
+      // the first parts are asked for along with the statistics
+      constexpr int kAhead = 4;
+      const int lg = c.D <= 128 ? 5 : 6, groups = kAttnThreads >> lg;
+      const int ch = min(4 * (tid & ((1 << lg) - 1)), c.D - 4), first = live.first + (tid >> lg);
+      auto part_at = [&](int s) { return *reinterpret_cast<const float4*>(p.part_o + (s * all + at) * c.D + ch); };
+      float4 v[kAhead];
+      float m[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int s = min(mine + i * groups, live.last);
-    v[i] = part_at(s);
-    m[i] = p.part_ml[s * all + at].x;
-  }
-  float top = -INFINITY;
-  for (int s = live.first + lane; s <= live.last; s += 64) top = fmaxf(top, p.part_ml[s * all + at].x);
+      for (int i = 0; i < kAhead; ++i) {
+        const int s = min(first + i * groups, live.last);
+        v[i] = part_at(s);
+        m[i] = p.part_ml[s * all + at].x;
+      }
+      float top = -INFINITY;
+      for (int s = live.first + lane; s <= live.last; s += 64) top = fmaxf(top, p.part_ml[s * all + at].x);
 #pragma unroll
-  for (int i = 32; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float total = 0.f;
-  for (int s = live.first + lane; s <= live.last; s += 64) {
-    const float2 ml = p.part_ml[s * all + at];
-    total = fmaf(fast_exp2(ml.x - ref), ml.y, total);
-  }
-  total = wave_sum(total);
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float4& x, float w) {
-    y.x = fmaf(w, x.x, y.x), y.y = fmaf(w, x.y, y.y), y.z = fmaf(w, x.z, y.z), y.w = fmaf(w, x.w, y.w);
-  };
+      for (int i = 32; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
+      const float ref = top == -INFINITY ? 0.f : top;
+      float total = 0.f;
+      for (int s = live.first + lane; s <= live.last; s += 64) {
+        const float2 ml = p.part_ml[s * all + at];
+        total = fmaf(fast_exp2(ml.x - ref), ml.y, total);
+      }
+      total = wave_sum(total);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](const float4& x, float w) {
+        y.x = fmaf(w, x.x, y.x), y.y = fmaf(w, x.y, y.y), y.z = fmaf(w, x.z, y.z), y.w = fmaf(w, x.w, y.w);
+      };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (mine + i * groups <= live.last) add(v[i], fast_exp2(m[i] - ref));
+      for (int i = 0; i < kAhead; ++i)
+        if (first + i * groups <= live.last) add(v[i], fast_exp2(m[i] - ref));
 #pragma unroll 4
-  for (int s = mine + kAhead * groups; s <= live.last; s += groups)
-    add(part_at(s), fast_exp2(p.part_ml[s * all + at].x - ref));
-  part[tid] = y;
-  __syncthreads();
-  if (tid >> lg) return;
-  for (int i = 1; i < groups; ++i) {
-    const float4 v = part[tid + (i << lg)];
-    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+      for (int s = first + kAhead * groups; s <= live.last; s += groups)
+        add(part_at(s), fast_exp2(p.part_ml[s * all + at].x - ref));
+      part[tid] = y;
+      __syncthreads();
+      if (tid >> lg == 0) {
+        for (int i = 1; i < groups; ++i) {
+          const float4 x = part[tid + (i << lg)];
+          y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        if (4 * tid < c.D)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + at / a.q_heads * a.out.token +
+                                    at % a.q_heads * a.out.head + ch) =
+              make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        if (a.lse && tid == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
+      }
+      __syncthreads();
+    }
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  if (4 * tid < c.D)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + ch) =
-        make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-  if (a.lse && tid == 0) a.lse[at] = total == 0.f ? -INFINITY : (ref + fast_log2(total)) * kLn2;
 }
 
+// Up to 4096 workgroups, twice what the card holds: where few of many rows were
+// split, a workgroup for each would cost more than the joining (164 thousand
+// rows: 250 us).
 template <int M>
 void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.num_splits == 1) return;
-  const dim3 grid(a.T * a.q_heads), block(kAttnThreads);
-  hipLaunchKernelGGL(join_kernel<M>, grid, block, 0, stream, a, p);
+  const int64_t all = int64_t(a.T) * a.q_heads;
+  const int per = int((all + 4095) / 4096);
+  const dim3 grid(int((all + per - 1) / per)), block(kAttnThreads);
+  hipLaunchKernelGGL(join_kernel<M>, grid, block, 0, stream, a, p, per);
 }
 
 template <int DP, int MT, bool FP8, bool SMALL>
@@ -1058,6 +1097,12 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   int64_t fine = groups > 0 ? 256 / groups : 1;
   fine = fine < (max_kv_len + 127) / 128 ? fine : (max_kv_len + 127) / 128;
   n = n > fine ? n : fine;
+  // Ranges of at most 16384 tokens, in up to 8 splits: a long context among
+  // many short ones does not wait for one workgroup then (one of 131000 tokens
+  // among 255 of 1000: 2.0 -> 0.65 ms; 256 of 1000 where 131000 are allowed for,
+  // 187 -> 225 us, where 32000 are, 194 us).
+  const int64_t ranges = (max_kv_len + 16383) / 16384 < 8 ? (max_kv_len + 16383) / 16384 : 8;
+  if (p.row_tile <= 32 && n < ranges) n = ranges;
   if (n < 1 || max_kv_len <= 512) n = 1;
   int64_t len = (max_kv_len + n - 1) / n;
   len = (len + 127) / 128 * 128;

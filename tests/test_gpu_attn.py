@@ -393,3 +393,23 @@ def test_attention_strides_of_dimensions_of_one():
     q1 = torch.randn((1, 1, 64), device="cuda").bfloat16()
     o = call(torch.as_strided(q1, (1, 1, 64), (777, 5, 1)), c, table, start, [70])
     check(o, q1, c, table, start, [70], 0.125)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("batch,new,heads,q_heads,D,window", [(300, 5, 2, 16, 64, 0), (70, 1, 8, 128, 128, 0),
+                                                             (260, 3, 4, 16, 256, 18000), (2200, 4, 4, 32, 16, 0)])
+def test_attention_of_a_few_long_contexts_among_many_short_ones(cache, batch, new, heads, q_heads, D, window):
+    """Few of the rows are split; requests without rows, of one, and with more than the hint says are among them."""
+    rng = np.random.default_rng(batch)
+    n = np.full(batch, new)
+    n[rng.integers(0, batch, 20)] = 0
+    n[rng.integers(0, batch, 10)] = 1
+    n[batch // 2] = new + 2
+    total = n + rng.integers(0, 40, batch)
+    total[[1, batch // 3, batch // 2, batch - 1]] += [17000, 33000, 20000, 9000]
+    pages, table, start = tables(n.tolist(), total.tolist(), 64, seed=batch)
+    c = fill(new_cache(cache, pages, 64, heads, D), batch)
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    q = torch.randn((start[-1], q_heads, D), generator=g, device="cuda").bfloat16()
+    o = call(q, c, table, start, total, window=window, max_q_len=new, max_kv_len=int(total.max()))
+    check(o, q, c, table, start, total, D ** -0.5, window)
