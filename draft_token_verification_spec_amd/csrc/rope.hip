@@ -5,8 +5,8 @@
 // position * freq[i].  The angle is formed in binary64, with the product's
 // rounding error carried along, as a number of turns (a position of 10^6 times
 // a frequency of 1 leaves binary32 no fraction); its whole turns are dropped
-// there, and cos and sin taken in binary32 of the remaining half turn at most
-// (absolute error below 1e-7).
+// there, and cos and sin taken in binary32 of the remaining half turn at most,
+// with what its rounding drops put back (an error near their own rounding's).
 //
 // One workgroup per row (new token): its rotary / 2 cos / sin pairs go to LDS
 // once and serve every head.  A group of 8, 16 or 32 lanes takes a head, a
@@ -35,13 +35,17 @@ constexpr int kMaxPairs = SV_ATTN_MAX_HEAD_DIM / 2;
 __device__ __forceinline__ void make_angles(float2* cs, const double* freq, int pairs, double position, float mscale,
                                             float sign) {
   constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLow = -9.839338337591243e-18;  // 1 / (2 pi) to 106 bits
+  constexpr double kPi = 3.141592653589793;
   for (int i = threadIdx.x; i < pairs; i += kRopeThreads) {
     const double f = freq[i], angle = position * f, low = fma(position, f, -angle);
     double turns = fma(angle, kInv2Pi, -rint(angle * kInv2Pi));
     turns += fma(angle, kInv2PiLow, low * kInv2Pi);
+    // what binary32 drops of the half turns is put back to first order
+    const double halves = 2 * turns;
+    const float near = float(halves), rest = float((halves - near) * kPi);
     float s, c;
-    sincospif(2.f * float(turns), &s, &c);
-    cs[i] = make_float2(c * mscale, s * mscale * sign);
+    sincospif(near, &s, &c);
+    cs[i] = make_float2(fmaf(-rest, s, c) * mscale, fmaf(rest, c, s) * mscale * sign);
   }
 }
 
