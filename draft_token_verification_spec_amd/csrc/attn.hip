@@ -24,7 +24,7 @@
 // through the wave's own part of LDS. A wave asks for the next block's keys
 // and values as soon as the present ones have left their registers. Measured:
 // 64 requests of 1024 to 4096 bf16 tokens, 8 heads of 128 channels, 677 MB
-// read in 136 us (5.0 TB/s, of which the paged rows alone read at 6.1 in a
+// read in 135 us (5.0 TB/s, of which the paged rows alone read at 6.1 in a
 // kernel that only loads); 256 requests of 500 to 2000 8-bit tokens, 5 new
 // tokens of 4 heads for each of 8, 689 MB in 149 us (4.6 TB/s). What is
 // missing to the read rate: a workgroup's start and end (5 to 7 us each, in
@@ -36,10 +36,10 @@
 // share tiles of 64 tokens, loaded a tile ahead into registers and staged in
 // two LDS buffers, so that a tile is read from memory once for 128 rows.
 // Measured: 2048 new tokens behind 8192, 32 heads of 128 channels over 8: 309
-// GFLOP in 323 to 334 us, 925 to 956 TFLOP/s (a library product of two 4096 x
+// GFLOP in 323 to 341 us, 907 to 956 TFLOP/s (a library product of two 4096 x
 // 4096 matrices: 1087); packed prompts of up to 4000 tokens at 64 channels
 // with a window of 2048, where a product has half the work for each
-// exponential: 580 to 596 TFLOP/s. With a tile of rows a request it is
+// exponential: 580 to 608 TFLOP/s. With a tile of rows a request it is
 // HBM-bound as well: 9 new tokens of 8 heads for each of 4 behind 131071, 4
 // requests, 1.07 GB in 211 us (5.1 TB/s). 32 rows of 256 channels are as fast
 // in either kernel for bf16 (72.8 and 74.9 us, 16 requests of 2048 tokens),
