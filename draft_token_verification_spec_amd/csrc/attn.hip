@@ -156,6 +156,11 @@ __device__ __forceinline__ uint32_t not_finite8(const uint4& w) {
   return (not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w)) & 0x80008000u;
 }
 
+// A value, or zeros.
+__device__ __forceinline__ uint4 only_if(bool keep, const uint4& w) {
+  return make_uint4(keep ? w.x : 0u, keep ? w.y : 0u, keep ? w.z : 0u, keep ? w.w : 0u);
+}
+
 // The larger of a value and that of the lane 32 away, or 16 and 32 away.
 __device__ __forceinline__ float max_over_halves(float x) {
   const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -275,7 +280,8 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
       }
     };
     // ask for a block's rows; the loads of absent tokens and of channels beyond
-    // the head's go to page 0 and to its last channels, and are not used
+    // the head's go to page 0 and to its last channels: the tokens are not seen,
+    // the keys' channels made zero, the values' not stored
     uint32_t lane_at[2][kLoads];  // bytes from the 16 tokens' first row, of keys and of values
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -313,6 +319,16 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
       request_values(base);
       pages(base + stride < end ? base + stride : base);
       do {
+        // the queries are zero beyond the head's channels, but zero times an infinite key would be NaN
+        if (c.D < DP) {
+          int beyond = lane >> 4;
+          asm volatile("" : "+v"(beyond));  // (masks formed here, not kept in registers through the loop)
+          beyond -= FP8 ? c.D >> 4 : c.D >> 3;
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) kr[h][i] = only_if(beyond + 4 * i < 0, kr[h][i]);
+        }
         // S^T, a block's 16 tokens by 16 rows at a time
         f32x4 s[2][MT];
 #pragma unroll
@@ -669,6 +685,13 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
     };
     auto stage_keys = [&](int buf) {
       uint16_t* const to = &keys[buf][tid / kLanes * kPitch<DP> + 8 * kParts * (tid % kLanes)];
+      // the queries are zero beyond the head's channels, but zero times an infinite key would be NaN
+      if (c.D < DP) {
+        int at = tid % kLanes;
+        asm volatile("" : "+v"(at));  // (the mask formed here, not kept in registers through the loop)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) kin[i] = only_if(at < (FP8 ? c.D >> 4 : c.D >> 3), kin[i]);
+      }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         if (FP8) {

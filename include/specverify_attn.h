@@ -185,6 +185,9 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  * value the channel's at least.  An infinite value that a row sees makes the
  * channel's result infinite or NaN, and may make the row's others and its lse
  * NaN.
+ * A score of -infinity (an infinite key) is a weight of zero, one of
+ * +infinity (or beyond binary32) makes its row NaN; a row whose weights are all
+ * zero gets what a row that sees no token gets.
  *   q, out     SV_BF16 elements, [T, q_heads, head_dim] with the given
  *              strides, 16-byte aligned, strides multiples of 8 elements (that
  *              of a dimension of one element is not looked at); no two of
