@@ -1095,6 +1095,7 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   const int G = q_heads / kv_heads;
   const int least = B > 0 ? (T + B - 1) / B : T;  // some request has that many rows
   max_q_len = max_q_len < least ? least : max_q_len > T ? T : max_q_len;
+  if (max_kv_len > SV_ATTN_MAX_TOKENS) max_kv_len = SV_ATTN_MAX_TOKENS;  // no page table holds more (and sums stay in 32 bits)
   const int64_t rows = int64_t(max_q_len) * G;
   p.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : kManyRows;
   // a request's tiles, as far as known; workgroups go on to further ones where
@@ -1129,7 +1130,7 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   if (n < 1 || max_kv_len <= 512) n = 1;
   int64_t len = (max_kv_len + n - 1) / n;
   len = (len + 127) / 128 * 128;
-  p.split_len = int(len < 128 ? 128 : len > (1 << 30) ? (1 << 30) : len);
+  p.split_len = int(len < 128 ? 128 : len);
   p.num_splits = int((int64_t(max_kv_len) + p.split_len - 1) / p.split_len);
   if (p.num_splits < 1) p.num_splits = 1;
   const size_t rows_all = size_t(T) * q_heads;
