@@ -1090,6 +1090,10 @@ void launch_dims(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
 
 }  // namespace
 
+// Bytes of divided contexts' parts.  (The rules that fill the card have at most
+// 1024 tiles of 128 rows, 2048 of 32 or 4096 of 16: a quarter of it at most.)
+constexpr size_t kMostParts = size_t(1) << 29;
+
 AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len) {
   AttnPlan p;
   const int G = q_heads / kv_heads;
@@ -1124,8 +1128,15 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   // Ranges of at most 16384 tokens, in up to 8 splits: a long context among
   // many short ones does not wait for one workgroup then (one of 131000 tokens
   // among 255 of 1000: 2.0 -> 0.65 ms; 256 of 1000 where 131000 are allowed for,
-  // 187 -> 225 us, where 32000 are, 194 us).
-  const int64_t ranges = (max_kv_len + 16383) / 16384 < 8 ? (max_kv_len + 16383) / 16384 : 8;
+  // 187 -> 225 us, where 32000 are, 194 us).  As many as their parts stay within
+  // kMostParts: with more rows the short contexts take as long as the long one
+  // (4096 requests of 5 tokens behind 700, 131000 allowed for: 2.7 GB of parts
+  // and 2.89 ms with 8 splits, 2.26 with none; one of 131000 among them 3.51
+  // and 3.88).
+  const size_t rows_all = size_t(T) * q_heads;
+  const size_t part_bytes = rows_all * (D * sizeof(float) + sizeof(float2));
+  int64_t ranges = (max_kv_len + 16383) / 16384 < 8 ? (max_kv_len + 16383) / 16384 : 8;
+  if (part_bytes * ranges > kMostParts) ranges = kMostParts / part_bytes;
   if (p.row_tile <= 32 && n < ranges) n = ranges;
   if (n < 1 || max_kv_len <= 512) n = 1;
   int64_t len = (max_kv_len + n - 1) / n;
@@ -1133,7 +1144,6 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   p.split_len = int(len < 128 ? 128 : len);
   p.num_splits = int((int64_t(max_kv_len) + p.split_len - 1) / p.split_len);
   if (p.num_splits < 1) p.num_splits = 1;
-  const size_t rows_all = size_t(T) * q_heads;
   p.ml_bytes = p.num_splits > 1 ? (size_t(p.num_splits) * rows_all * sizeof(float2) + 255) / 256 * 256 : 0;
   p.o_bytes = p.num_splits > 1 ? (size_t(p.num_splits) * rows_all * D * sizeof(float) + 255) / 256 * 256 : 0;
   p.part_ml = nullptr;

@@ -169,7 +169,7 @@ int sv_kv_gather(void* stream, int B, int T, int out_dtype, const sv_paged_cache
 
 /* Bytes of workspace that sv_paged_attention needs for these sizes: 256 stands
  * for none (no context is split; the call then takes a NULL workspace), 0 for
- * sizes that the call would reject. */
+ * sizes that the call would reject.  At most 2^29 + 1024. */
 size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim, int max_q_len,
                                          int max_kv_len);
 

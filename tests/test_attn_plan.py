@@ -1,6 +1,8 @@
 """How sv_paged_attention divides its work, as far as its workspace's size tells
 (no GPU)."""
+import math
 import os
+import random
 
 import pytest
 
@@ -19,3 +21,21 @@ def test_longest_hint_is_the_largest_cache(batch, rows, q_heads, heads, D, max_q
     sizes = [sv.sv_paged_attention_workspace_size(batch, rows, q_heads, heads, D, max_q, kv)
              for kv in (sv.SV_ATTN_MAX_TOKENS, sv.SV_ATTN_MAX_TOKENS + 1, INT_MAX - 300, INT_MAX - 16000, INT_MAX)]
     assert len(set(sizes)) == 1, sizes
+
+
+def test_scratch_is_bounded():
+    """Parts of divided contexts take at most 2^29 bytes, however many rows, long contexts or loose hints a call has."""
+    size = sv.sv_paged_attention_workspace_size
+    rng = random.Random(1)
+    log = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    cases = [(4096, 20480, 32, 8, 128, 5, 131072), (4096, 20480, 32, 8, 128, 0, 131072), (1 << 18, 1 << 20, 128, 8, 256, 1, 1 << 30),
+             (1 << 18, 1 << 21, 1023, 1, 16, 0, INT_MAX), (1, 1, 1024, 1024, 256, 1, INT_MAX)]
+    for _ in range(20000):
+        heads = log(1, 64)
+        q_heads = heads * log(1, 1024 // heads)
+        batch, rows = log(1, 1 << 18), log(1, min(1 << 23, INT_MAX // q_heads))
+        cases.append((batch, rows, q_heads, heads, 16 * log(1, 16), rng.choice([0, 1, 5, log(1, rows)]), log(1, INT_MAX)))
+    for case in cases:
+        assert 256 <= size(*case) <= (1 << 29) + 1024, case
+    # and a context among few enough is still divided
+    assert size(256, 1280, 32, 8, 128, 5, 131072) > 8 * 1280 * 32 * 128 * 4
