@@ -132,7 +132,14 @@ def _three(name: str, t: torch.Tensor) -> tuple:
     shape = t.shape
     if len(shape) != 3:
         raise ValueError(f"{name} must be [rows, heads, head_dim] (got {list(shape)})")
+    if shape[0] > SV_ATTN_MAX_ROWS:
+        raise ValueError(f"{name} has {shape[0]} rows, a call has at most {SV_ATTN_MAX_ROWS}")
     return shape
+
+
+def _wide(n: int) -> int:
+    """A window or hint as the C call's int, which would wrap around: what is beyond it says no more than its ends."""
+    return n if -1 <= n <= 0x7FFFFFFF else 0x7FFFFFFF if n > 0 else -1
 
 
 def _new(shape: tuple, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
@@ -335,6 +342,8 @@ def sv_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     kb = None if kv_begin is None else _array(dev, "kv_begin", kv_begin, torch.int32, (B,))
     code = _dtype_code("dtype", dtype)
     o = {} if out is None else out
+    if rows > SV_ATTN_MAX_ROWS:
+        raise ValueError(f"{rows} rows, a call has at most {SV_ATTN_MAX_ROWS}")
     shape = (rows, heads, D)
     ptr = []
     for name in ("k", "v"):
@@ -350,8 +359,8 @@ def sv_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
 @functools.lru_cache(maxsize=4096)
 def sv_paged_attention_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int = 0,
                                       max_kv_len: int = 0) -> int:
-    return int(_attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, kv_heads, head_dim, max_q_len,
-                                                             max_kv_len))
+    return int(_attn_lib().sv_paged_attention_workspace_size(B, T, q_heads, kv_heads, head_dim, _wide(max_q_len),
+                                                             _wide(max_kv_len)))
 
 
 def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
@@ -404,6 +413,6 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         ws = workspace
         _array(dev, "workspace", ws, torch.uint8, (ws.numel(),))
         nbytes = ws.numel()
-    _call(dev, "sv_paged_attention", B, T, q_heads, *qr, cache, qs, kl, max_q_len, max_kv_len,
-          D ** -0.5 if scale is None else scale, window, *orows, lse, None if ws is None else ws.data_ptr(), nbytes)
+    _call(dev, "sv_paged_attention", B, T, q_heads, *qr, cache, qs, kl, _wide(max_q_len), _wide(max_kv_len),
+          D ** -0.5 if scale is None else scale, _wide(window), *orows, lse, None if ws is None else ws.data_ptr(), nbytes)
     return o

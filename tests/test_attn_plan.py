@@ -3,6 +3,7 @@
 import math
 import os
 import random
+import sys
 
 import pytest
 
@@ -39,3 +40,14 @@ def test_scratch_is_bounded():
         assert 256 <= size(*case) <= (1 << 29) + 1024, case
     # and a context among few enough is still divided
     assert size(256, 1280, 32, 8, 128, 5, 131072) > 8 * 1280 * 32 * 128 * 4
+
+
+def test_hints_beyond_32_bits():
+    """Python's integers have no end; a hint of any size says what the largest says."""
+    size = sv.sv_paged_attention_workspace_size
+    want = size(8, 8, 32, 8, 128, 1, INT_MAX)
+    assert want > 256
+    for kv in (1 << 31, (1 << 32) + 5, 1 << 40, sys.maxsize):
+        assert size(8, 8, 32, 8, 128, 1, kv) == want
+        assert size(8, 8, 32, 8, 128, kv, INT_MAX) == size(8, 8, 32, 8, 128, 8, INT_MAX)
+    assert size(8, 8, 32, 8, 128, 1, -1) == size(8, 8, 32, 8, 128, 1, 5 - (1 << 32)) == 0
