@@ -237,7 +237,7 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
   if (st != SV_OK) return st;
   st = check_attention_sizes(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
   if (st != SV_OK) return st;
-  if (!(scale > 0.f) || !isfinite(scale) || window < 0) return SV_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f) || window < 0) return SV_ERR_INVALID_ARG;
   if (empty) return SV_OK;
   if (!q || !out || !query_start || !kv_len || !aligned16(q) || !aligned16(out)) return SV_ERR_INVALID_ARG;
   for (int64_t s : {q_token_stride, out_token_stride})

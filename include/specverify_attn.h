@@ -186,15 +186,16 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  * channel's result infinite or NaN, and may make the row's others and its lse
  * NaN.
  * A score of -infinity (an infinite key) is a weight of zero, one of
- * +infinity (or beyond binary32) makes its row NaN; a row whose weights are all
- * zero gets what a row that sees no token gets.
+ * +infinity makes its row NaN; a row whose weights are all zero gets what a row
+ * that sees no token gets.  Scores are formed in binary32 and in base 2:
+ * finite ones of 2.3e38 and more give no meaningful row.
  *   q, out     SV_BF16 elements, [T, q_heads, head_dim] with the given
  *              strides, 16-byte aligned, strides multiples of 8 elements (that
  *              of a dimension of one element is not looked at); no two of
  *              out's rows may overlap.  q_heads a multiple of cache->heads,
  *              T * q_heads below 2^31.
  *   lse        float [T, q_heads], or NULL.
- *   scale      > 0 and finite (usually head_dim^-0.5).
+ *   scale      > 0 and below 2.35e38 (usually head_dim^-0.5).
  *   max_q_len, max_kv_len   the most new tokens of a request and the largest
  *              kv_len, as far as the caller knows them (0: not known): they
  *              choose how the work is divided and change results by rounding

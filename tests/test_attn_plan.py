@@ -51,3 +51,11 @@ def test_hints_beyond_32_bits():
         assert size(8, 8, 32, 8, 128, 1, kv) == want
         assert size(8, 8, 32, 8, 128, kv, INT_MAX) == size(8, 8, 32, 8, 128, 8, INT_MAX)
     assert size(8, 8, 32, 8, 128, 1, -1) == size(8, 8, 32, 8, 128, 1, 5 - (1 << 32)) == 0
+
+
+@pytest.mark.parametrize("scale,status", [(2.3e38, 0), (2.36e38, -1), (3.4e38, -1), (1e-45, 0), (0.0, -1)])
+def test_scale_in_base_two_is_finite(scale, status):
+    """Scores are formed in base 2: a scale that is infinite there is refused (no row: what is let pass does nothing)."""
+    from test_attn_abi import attention
+
+    assert attention(T=0, scale=scale) == status
