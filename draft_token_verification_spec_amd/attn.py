@@ -375,6 +375,12 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     0: every earlier token.  Returns ``out`` (as q) and, if asked for, ``lse``
     float32 [T, q_heads]; rows of no request are not written.
 
+    ``max_q_len``, ``max_kv_len``: the most new tokens of a request and the
+    longest context, where known.  They change times, not results: without the
+    first a request of far more rows than the average is slow, without the second
+    (default: the page table's width) contexts are divided for the longest one
+    that the table could hold.
+
     Without a ``workspace`` the call takes one from torch's allocator for its
     own duration: calls on different streams, and captured graphs, then share
     nothing.  Else a contiguous uint8 tensor of at least

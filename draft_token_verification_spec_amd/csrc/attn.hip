@@ -36,14 +36,14 @@
 // share tiles of 64 tokens, loaded a tile ahead into registers and staged in
 // two LDS buffers, so that a tile is read from memory once for 128 rows.
 // Measured: 2048 new tokens behind 8192, 32 heads of 128 channels over 8: 309
-// GFLOP in 323 to 341 us, 907 to 956 TFLOP/s (a library product of two 4096 x
-// 4096 matrices: 1087); packed prompts of up to 4000 tokens at 64 channels
-// with a window of 2048, where a product has half the work for each
-// exponential: 580 to 608 TFLOP/s. With a tile of rows a request it is
-// HBM-bound as well: 9 new tokens of 8 heads for each of 4 behind 131071, 4
-// requests, 1.07 GB in 211 us (5.1 TB/s). 32 rows of 256 channels are as fast
-// in either kernel for bf16 (72.8 and 74.9 us, 16 requests of 2048 tokens),
-// but not for 8-bit caches (46.8 and 67.0 us).
+// GFLOP in 331 to 336 us, 920 to 934 TFLOP/s (library products of two 4096 x
+// 4096 and two 8192 x 8192 matrices: 1087 and 1278); packed prompts of up to
+// 4000 tokens at 64 channels with a window of 2048, where a product has half
+// the work for each exponential: 612 TFLOP/s. With a tile of rows a request it
+// is HBM-bound as well: 9 new tokens of 8 heads for each of 4 behind 131071, 4
+// requests, 1.07 GB in 213 us (5.0 TB/s). 20 rows of 256 channels (5 tokens of
+// 4 heads) are about as fast in either kernel for bf16 (72.8 and 74.9 us, 16
+// requests of 2048 tokens), but not for 8-bit caches (46.8 and 67.0 us).
 //
 // Splits: where rows are few and contexts long, a context is divided into
 // ranges of `split_len` tokens, whose results (running maximum, sum, weighted

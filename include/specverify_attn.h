@@ -82,8 +82,8 @@ typedef struct {
   int64_t k_page_stride, k_token_stride, k_head_stride;
   int64_t v_page_stride, v_token_stride, v_head_stride;
   uint8_t* k_scale; /* SV_E4M3: uint8 [num_pages, heads, page_size], the    */
-  uint8_t* v_scale; /* biased exponent e + 127 of each row's scale 2^e;     */
-                    /* SV_BF16: not read, may be NULL                       */
+  uint8_t* v_scale; /* biased exponent e + 127 of each row's scale 2^e (255: */
+                    /* the row is NaN); SV_BF16: not read, may be NULL      */
 } sv_paged_cache;
 
 /* Layouts of the turned channels: pair i of `rotary_dim / 2` is channels
@@ -192,17 +192,24 @@ size_t sv_paged_attention_workspace_size(int B, int T, int q_heads, int kv_heads
  *   q, out     SV_BF16 elements, [T, q_heads, head_dim] with the given
  *              strides, 16-byte aligned, strides multiples of 8 elements (that
  *              of a dimension of one element is not looked at); no two of
- *              out's rows may overlap.  q_heads a multiple of cache->heads,
- *              T * q_heads below 2^31.
+ *              out's rows may overlap, nor out and q.  q_heads a multiple of
+ *              cache->heads, T * q_heads below 2^31.
  *   lse        float [T, q_heads], or NULL.
  *   scale      > 0 and below 2.35e38 (usually head_dim^-0.5).
  *   max_q_len, max_kv_len   the most new tokens of a request and the largest
  *              kv_len, as far as the caller knows them (0: not known): they
  *              choose how the work is divided and change results by rounding
- *              only; larger requests are computed all the same.
+ *              only; larger requests are computed all the same.  Without
+ *              max_q_len the average T / B is taken, and a request of more rows
+ *              is worked off a tile after the other by the workgroups that an
+ *              average one has: a prompt among decoding requests takes several
+ *              times as long as with it.  Without max_kv_len no context is
+ *              divided; a loose one costs workgroups and scratch.
  *   workspace  scratch of this call alone, 16-byte aligned; not a workspace of
  *              specverify.h's calls, whose cleared part it would overwrite.
- * Scores, sums and outputs are accumulated in binary32. */
+ * Scores, sums and outputs are accumulated in binary32; the weights w_j are
+ * rounded to bf16 for their product with the values (by up to 2^-8 of each; lse
+ * and the sum that out is divided by have them unrounded). */
 int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
                        int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
                        const int32_t* kv_len, int max_q_len, int max_kv_len, float scale, int window, void* out,
