@@ -53,3 +53,30 @@ def test_attention_of_scores_of_minus_infinity_alone(D, new, total):
     q[..., D - 1] = 0.5
     o = call(q, c, table, start, [total], max_kv_len=total)
     assert (o["out"] == 0).all() and torch.isneginf(o["lse"]).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [4, 16, 64])
+@pytest.mark.parametrize("new,q_heads,total", [(1, 4, 37), (7, 4, 1500), (40, 4, 175)])
+@pytest.mark.parametrize("D", [48, 80, 240])
+def test_padded_heads_ignore_what_they_do_not_see(D, new, q_heads, total, page, cache):
+    """NaN and infinities behind the end, before the window and on other pages change nothing at padded sizes either."""
+    window = 30
+    pages, table, start = tables([new], [total], page, spare=3, seed=D)
+    c = fill(new_cache(cache, pages, page, 1, D), D)
+    q = torch.randn((new, q_heads, D), device="cuda").bfloat16()
+    kw = dict(window=window, max_q_len=new, max_kv_len=total)
+    clean = call(q, c, table, start, [total], **kw)
+    assert torch.isfinite(clean["out"]).all()
+    seen = torch.zeros((pages, page), dtype=torch.bool)
+    for j in range(max(0, total - new - window + 1), total):
+        seen[int(table[0, j // page]), j % page] = True
+    hidden = (~seen).nonzero().cuda()
+    for bad in (float("nan"), float("inf"), float("-inf")) if cache == "bf16" else (float("nan"),):
+        for n in ("k", "v"):
+            x = c[n + "_cache"]
+            some = torch.full((len(hidden), 1, D), bad, device="cuda").to(x.dtype)
+            bits = torch.int16 if cache == "bf16" else torch.uint8
+            x.view(bits)[hidden[:, 0], hidden[:, 1]] = some.view(bits)
+        got = call(q, c, table, start, [total], **kw)
+        assert torch.equal(got["out"], clean["out"]) and torch.equal(got["lse"], clean["lse"])
