@@ -31,7 +31,13 @@ __all__ = [
     "SV_ROPE_SCALINGS",
     "sv_rope_frequencies",
     "sv_rope",
+    "sv_qk_norm_rope",
+    "sv_qk_norm_rope_backward",
+    "sv_qk_norm_rope_backward_workspace_size",
     "sv_kv_append",
+    "sv_kv_append_normed",
+    "sv_kv_pages",
+    "sv_kv_pages_workspace_size",
     "sv_kv_gather",
     "sv_paged_attention",
     "sv_paged_attention_workspace_size",
@@ -59,6 +65,16 @@ _SIGNATURES = {
     "sv_rope": (_i, [_p, _i, _i, _i, _i, _i, _i, _i, _p, _i64, _i64, _p, _p, _f, _p, _i64, _i64]),
     "sv_kv_append": (_i, [_p, _i, _i, _i, _i, _i, _i, _p, _f, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p,
                           _i64, _i64, _p, _p, _p]),
+    "sv_qk_norm_rope": (_i, [_p, _i, _i, _i, _i, _i, _i, _i, _p, _i64, _i64, _p, _i64, _i64, _i, _p, _p, _f, _p, _p, _f,
+                             _p, _i64, _i64, _p, _i64, _i64]),
+    "sv_qk_norm_rope_backward_workspace_size": (_sz, [_i, _i]),
+    "sv_qk_norm_rope_backward": (_i, [_p, _i, _i, _i, _i, _i, _i, _i, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64,
+                                      _p, _i64, _i64, _i, _p, _p, _f, _p, _p, _f, _p, _i64, _i64, _p, _i64, _i64, _p,
+                                      _p, _p, _sz]),
+    "sv_kv_append_normed": (_i, [_p, _i, _i, _i, _i, _i, _i, _p, _f, _p, _i, _p, _p, _f, _p, _i64, _i64, _p, _i64, _i64,
+                                 _p, _i64, _i64, _p, _i64, _i64, _p, _p, _p]),
+    "sv_kv_pages_workspace_size": (_sz, [_i, _i]),
+    "sv_kv_pages": (_i, [_p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _sz]),
     "sv_kv_gather": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _p]),
     "sv_paged_attention_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "sv_paged_attention": (_i, [_p, _i, _i, _i, _p, _i64, _i64, _p, _p, _p, _i, _i, _f, _i, _p, _i64, _i64, _p, _p,
@@ -174,6 +190,28 @@ def _freq(dev: int, freq: Optional[torch.Tensor]):
     return freq.data_ptr(), 2 * freq.shape[0]
 
 
+def _weights(dev: int, D: int, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor]):
+    """(type, addresses) of the weights of queries' and keys' norms."""
+    some = k_weight if q_weight is None else q_weight
+    if some is None:
+        return SV_F32, None, None
+    _tensor("k_weight" if q_weight is None else "q_weight", some)
+    dtype = some.dtype
+    code = _dtype_code("the norms' weights", dtype)
+    return (code, None if q_weight is None else _array(dev, "q_weight", q_weight, dtype, (D,)),
+            None if k_weight is None else _array(dev, "k_weight", k_weight, dtype, (D,)))
+
+
+def _scratch(dev: int, nbytes: int, workspace: Optional[torch.Tensor], device: torch.device):
+    """(tensor to be kept until the call returns, its bytes): the caller's, or one of `nbytes` (256: none)."""
+    if workspace is not None:
+        _array(dev, "workspace", workspace, torch.uint8, (workspace.numel(),))
+        return workspace, workspace.numel()
+    if nbytes <= 256:
+        return None, nbytes
+    return torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device), nbytes
+
+
 # sv_paged_cache, as bytes: heads and head_dim are fields 1 and 2, max_pages and page_size 5 and 3
 _CACHE = struct.Struct("@6iPqPP6qPP")
 
@@ -282,17 +320,116 @@ def sv_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, lay
     return out
 
 
-def sv_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                 page_table: torch.Tensor, query_start: torch.Tensor, kv_len: torch.Tensor, *,
-                 q: Optional[torch.Tensor] = None, freq: Optional[torch.Tensor] = None, layout: str = "half",
-                 mscale: float = 1.0, positions: Optional[torch.Tensor] = None,
-                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
-                 out: Optional[dict] = None) -> dict:
-    """Append the new tokens' keys and values ``k``, ``v`` [T, heads, head_dim]
-    (bfloat16 or float32) to a paged cache, in place, keys turned by their
-    positions if ``freq`` is given; see ``sv_kv_append``.  ``q`` [T, q_heads,
-    head_dim]: queries to turn likewise, returned as ``q`` (rows of no request
-    are not written).  ``positions`` int64 [T], default: the tokens' places."""
+def _two(dev: int, name: str, q, k, T: int, D: int, dtype):
+    """Rows of queries and keys (no keys: k is None): (q, its heads, k, its heads)."""
+    q_heads = q.shape[1]
+    qr = _rows(dev, name.format("q"), q, dtype, (T, q_heads, D))
+    if k is None:
+        return qr, q_heads, (None, 0, 0), 0
+    _tensor(name.format("k"), k)
+    k_heads = _three(name.format("k"), k)[1]
+    return qr, q_heads, _rows(dev, name.format("k"), k, dtype, (T, k_heads, D)), k_heads
+
+
+def _outputs(dev: int, o: dict, names, like, T: int, D: int, dtype):
+    """Rows of the named outputs, each as one of `like` (None: no such output), made where the dict lacks them."""
+    rows = []
+    for name, x in zip(names, like):
+        if x is None:
+            rows.append((None, 0, 0))
+            continue
+        shape = (T, x.shape[1], D)
+        if name in o:
+            rows.append(_rows(dev, f"out['{name}']", o[name], dtype, shape))
+        else:
+            t = o[name] = _new(shape, dtype, x.device)
+            rows.append((t.data_ptr(), shape[1] * D, D))
+    return rows
+
+
+def _turns(dev: int, T: int, positions, freq):
+    """(positions, frequencies, turned channels); without frequencies nothing is turned."""
+    fp, rotary = _freq(dev, freq)
+    if rotary == 0:
+        return None, None, 0
+    if positions is None:
+        raise ValueError("positions are needed where freq is given")
+    return _array(dev, "positions", positions, torch.int64, (T,)), fp, rotary
+
+
+def sv_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                    freq: Optional[torch.Tensor] = None, *, q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, layout: str = "half",
+                    mscale: float = 1.0, out: Optional[dict] = None) -> dict:
+    """Norms of the heads of queries ``q`` [T, q_heads, head_dim] and keys ``k``
+    [T, k_heads, head_dim] (None: no keys; bfloat16 or float32) and their rotary
+    positions in one pass; see ``sv_qk_norm_rope``.  ``q_weight``, ``k_weight``
+    [head_dim] (bfloat16 or float32, both alike), default: all 1; ``positions``
+    int64 [T] and ``freq`` as for ``sv_rope``, without ``freq`` nothing is turned.
+    Returns ``q`` and ``k``; ``out`` may hold the inputs themselves."""
+    dev = _tensor("q", q)
+    T, _, D = _three("q", q)
+    dtype = q.dtype
+    code = _dtype_code("q", dtype)
+    qr, q_heads, kr, k_heads = _two(dev, "{}", q, k, T, D, dtype)
+    pos, fp, rotary = _turns(dev, T, positions, freq)
+    weights = _weights(dev, D, q_weight, k_weight)
+    o = {} if out is None else out
+    qo, ko = _outputs(dev, o, ("q", "k"), (q, k), T, D, dtype)
+    _call(dev, "sv_qk_norm_rope", T, q_heads, k_heads, D, rotary, _layout(layout), code, *qr, *kr, *weights, eps, pos, fp,
+          mscale, *qo, *ko)
+    return o
+
+
+@functools.lru_cache(maxsize=4096)
+def sv_qk_norm_rope_backward_workspace_size(T: int, head_dim: int) -> int:
+    return int(_attn_lib().sv_qk_norm_rope_backward_workspace_size(T, head_dim))
+
+
+def sv_qk_norm_rope_backward(q: torch.Tensor, k: Optional[torch.Tensor], dq_out: torch.Tensor,
+                             dk_out: Optional[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                             freq: Optional[torch.Tensor] = None, *, q_weight: Optional[torch.Tensor] = None,
+                             k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, layout: str = "half",
+                             mscale: float = 1.0, want_weights: bool = True,
+                             workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+    """The gradients of ``sv_qk_norm_rope`` from ``dq_out``, ``dk_out``, those
+    with respect to its outputs; see ``sv_qk_norm_rope_backward``.  Returns
+    ``dq``, ``dk`` (of q's type) and, if ``want_weights``, ``dq_weight``,
+    ``dk_weight`` float32 [head_dim] (of missing weights too, which are all 1)."""
+    dev = _tensor("q", q)
+    T, _, D = _three("q", q)
+    dtype = q.dtype
+    code = _dtype_code("q", dtype)
+    qr, q_heads, kr, k_heads = _two(dev, "{}", q, k, T, D, dtype)
+    _tensor("dq_out", dq_out)
+    _three("dq_out", dq_out)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    gqr, gq_heads, gkr, gk_heads = _two(dev, "d{}_out", dq_out, dk_out, T, D, dtype)
+    if gq_heads != q_heads or gk_heads != k_heads:
+        raise ValueError(f"dq_out and dk_out have {gq_heads} and {gk_heads} heads, q and k {q_heads} and {k_heads}")
+    pos, fp, rotary = _turns(dev, T, positions, freq)
+    weights = _weights(dev, D, q_weight, k_weight)
+    o = {} if out is None else out
+    qo, ko = _outputs(dev, o, ("dq", "dk"), (q, k), T, D, dtype)
+    dw = [None, None]
+    for i, (name, x) in enumerate((("dq_weight", q), ("dk_weight", k))):
+        if name in o:
+            dw[i] = _array(dev, f"out['{name}']", o[name], torch.float32, (D,))
+        elif want_weights and x is not None:
+            o[name] = torch.empty_strided((D,), (1,), dtype=torch.float32, device=q.device)
+            dw[i] = o[name].data_ptr()
+    ws, nbytes = None, 0
+    if dw != [None, None]:
+        ws, nbytes = _scratch(dev, sv_qk_norm_rope_backward_workspace_size(T, D), workspace, q.device)
+    _call(dev, "sv_qk_norm_rope_backward", T, q_heads, k_heads, D, rotary, _layout(layout), code, *qr, *kr, *gqr, *gkr,
+          *weights, eps, pos, fp, mscale, *qo, *ko, *dw, None if ws is None else ws.data_ptr(), nbytes)
+    return o
+
+
+def _append(what: str, k, v, k_cache, v_cache, page_table, query_start, kv_len, q, freq, layout, mscale, positions,
+            k_scale, v_scale, out, norm) -> dict:
+    """sv_kv_append, or sv_kv_append_normed with ``norm`` (q_weight, k_weight, eps)."""
     dev = _tensor("k", k)
     shape = T, heads, D = _three("k", k)
     _tensor("kv_len", kv_len)
@@ -319,8 +456,99 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         else:
             o["q"] = _new((T, q_heads, D), dtype, q.device)
             qo = o["q"].data_ptr(), q_heads * D, D
-    _call(dev, "sv_kv_append", B, T, q_heads, code, rotary, _layout(layout), fp, mscale, pos, *qr, *qo, *kr, *vr, qs,
-          kl, cache)
+    norms = () if norm is None else (*_weights(dev, D, norm[0], norm[1]), norm[2])
+    _call(dev, what, B, T, q_heads, code, rotary, _layout(layout), fp, mscale, pos, *norms, *qr, *qo, *kr, *vr, qs, kl,
+          cache)
+    return o
+
+
+def sv_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 page_table: torch.Tensor, query_start: torch.Tensor, kv_len: torch.Tensor, *,
+                 q: Optional[torch.Tensor] = None, freq: Optional[torch.Tensor] = None, layout: str = "half",
+                 mscale: float = 1.0, positions: Optional[torch.Tensor] = None,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 out: Optional[dict] = None) -> dict:
+    """Append the new tokens' keys and values ``k``, ``v`` [T, heads, head_dim]
+    (bfloat16 or float32) to a paged cache, in place, keys turned by their
+    positions if ``freq`` is given; see ``sv_kv_append``.  ``q`` [T, q_heads,
+    head_dim]: queries to turn likewise, returned as ``q`` (rows of no request
+    are not written).  ``positions`` int64 [T], default: the tokens' places."""
+    return _append("sv_kv_append", k, v, k_cache, v_cache, page_table, query_start, kv_len, q, freq, layout, mscale,
+                   positions, k_scale, v_scale, out, None)
+
+
+def sv_kv_append_normed(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        page_table: torch.Tensor, query_start: torch.Tensor, kv_len: torch.Tensor, *,
+                        q: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        freq: Optional[torch.Tensor] = None, layout: str = "half", mscale: float = 1.0,
+                        positions: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                        v_scale: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+    """``sv_kv_append`` with each key and query head's row normed before it is
+    turned; see ``sv_kv_append_normed``.  ``q_weight``, ``k_weight`` [head_dim]
+    (bfloat16 or float32, both alike), default: all 1."""
+    return _append("sv_kv_append_normed", k, v, k_cache, v_cache, page_table, query_start, kv_len, q, freq, layout, mscale,
+                   positions, k_scale, v_scale, out, (q_weight, k_weight, eps))
+
+
+@functools.lru_cache(maxsize=4096)
+def sv_kv_pages_workspace_size(B: int, T: int = 0) -> int:
+    return int(_attn_lib().sv_kv_pages_workspace_size(B, T))
+
+
+def sv_kv_pages(page_table: torch.Tensor, pages_held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                kv_len: torch.Tensor, *, page_size: int, shared_pages: Optional[torch.Tensor] = None,
+                query_start: Optional[torch.Tensor] = None, rows: int = 0, workspace: Optional[torch.Tensor] = None,
+                out: Optional[dict] = None) -> dict:
+    """Pages of a cache taken and given back, in place, so that each request
+    holds what its length needs; see ``sv_kv_pages``.  ``page_table`` int32 [B,
+    max_pages] (-1 from ``pages_held`` on), ``pages_held``, ``kv_len`` and
+    ``shared_pages`` int32 [B], ``free_pages`` int32 [pages of the cache] with
+    the first ``free_count`` int32 [1] of them free.  Returns ``granted`` int32
+    [B] and, with ``query_start`` int32 [B + 1] of ``rows`` new tokens, ``slots``
+    and ``positions`` int64 [rows] (rows of no request are not written)."""
+    dev = _tensor("page_table", page_table)
+    _tensor("kv_len", kv_len)
+    B = kv_len.numel()
+    if page_table.dtype != torch.int32:
+        _refuse(dev, "page_table", page_table, torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages] (got {list(page_table.shape)})")
+    max_pages = page_table.shape[1]
+    stride, one = page_table.stride()
+    if one != 1 and max_pages > 1:
+        raise ValueError("page_table must have unit stride along the pages")
+    if B <= 1:
+        stride = max_pages
+    _tensor("free_pages", free_pages)
+    num_pages = free_pages.numel()
+    if num_pages > 0x7FFFFFFF:
+        raise ValueError(f"free_pages has {num_pages} entries, a cache has fewer than 2^31 pages")
+    held = _array(dev, "pages_held", pages_held, torch.int32, (B,))
+    free = _array(dev, "free_pages", free_pages, torch.int32, (num_pages,))
+    count = _array(dev, "free_count", free_count, torch.int32, (1,))
+    kl = _array(dev, "kv_len", kv_len, torch.int32, (B,))
+    shared = None if shared_pages is None else _array(dev, "shared_pages", shared_pages, torch.int32, (B,))
+    if not 0 <= rows <= SV_ATTN_MAX_ROWS:
+        raise ValueError(f"{rows} rows, a call has at most {SV_ATTN_MAX_ROWS}")
+    o = {} if out is None else out
+    device = page_table.device
+    ptr = {}
+    names = [("granted", torch.int32, B)]
+    if query_start is not None:
+        names += [("slots", torch.int64, rows), ("positions", torch.int64, rows)]
+        qs = _array(dev, "query_start", query_start, torch.int32, (B + 1,))
+    else:
+        qs, rows = None, 0
+    for name, dtype, n in names:
+        if name in o:
+            ptr[name] = _array(dev, f"out['{name}']", o[name], dtype, (n,))
+        else:
+            t = o[name] = torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+            ptr[name] = t.data_ptr()
+    ws, nbytes = _scratch(dev, sv_kv_pages_workspace_size(B, rows), workspace, device)
+    _call(dev, "sv_kv_pages", B, rows, page_size, max_pages, num_pages, kl, shared, qs, page_table.data_ptr(), stride, held,
+          free, count, ptr["granted"], ptr.get("slots"), ptr.get("positions"), None if ws is None else ws.data_ptr(), nbytes)
     return o
 
 

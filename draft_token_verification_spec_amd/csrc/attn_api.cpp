@@ -90,6 +90,74 @@ int check_attention_sizes(int B, int T, int q_heads, int kv_heads, int head_dim,
   return SV_OK;
 }
 
+// A norm's arguments; rows are checked by row_strides_ok.
+bool norm_ok(int weight_dtype, float eps) { return rows_dtype_ok(weight_dtype) && eps > 0.f && isfinite(eps); }
+
+int append(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, int layout, const double* freq,
+           float mscale, const int64_t* positions, const NormWeights* norm, const RowsIn& q, const RowsOut& q_out,
+           const RowsIn& k, const RowsIn& v, const int32_t* query_start, const int32_t* kv_len,
+           const sv_paged_cache* cache) {
+  int st = check_batch(B, T);
+  if (st != SV_OK) return st;
+  const bool empty = B == 0 || T == 0;
+  st = check_cache(cache, B, empty);
+  if (st != SV_OK) return st;
+  if (q_heads < 0 || !rows_dtype_ok(dtype) || rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > cache->head_dim ||
+      (layout != SV_ROPE_HALF && layout != SV_ROPE_INTERLEAVED) || !isfinite(mscale) ||
+      (norm && !norm_ok(norm->dtype, norm->eps)))
+    return SV_ERR_INVALID_ARG;
+  if (q_heads > SV_ATTN_MAX_HEADS) return SV_ERR_UNSUPPORTED;
+  if (empty) return SV_OK;
+  if (!k.p || !v.p || !query_start || !kv_len || (rotary_dim > 0 && !freq) || (q_heads > 0 && (!q.p || !q_out.p)))
+    return SV_ERR_INVALID_ARG;
+  if (!read_strides_ok(k.token, k.head) || !read_strides_ok(v.token, v.head)) return SV_ERR_INVALID_ARG;
+  if (q_heads > 0 && (!read_strides_ok(q.token, q.head) ||
+                      !write_strides_ok(T, q_heads, cache->head_dim, q_out.token, q_out.head)))
+    return SV_ERR_INVALID_ARG;
+  AppendArgs a;
+  a.B = B;
+  a.T = T;
+  a.q_heads = q_heads;
+  a.rotary = rotary_dim;
+  a.layout = layout;
+  a.freq = freq;
+  a.mscale = mscale;
+  a.positions = positions;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.query_start = query_start;
+  a.kv_len = kv_len;
+  a.cache = view_of(cache);
+  a.normed = norm != nullptr;
+  a.norm = norm ? *norm : NormWeights{nullptr, nullptr, SV_F32, 1.f};
+  return to_status(launch_append(a, dtype, cache->dtype, static_cast<hipStream_t>(stream)));
+}
+
+// Sizes, types and pointers of sv_qk_norm_rope and its backward pass;
+// SV_OK with a.T set to 0 if there is nothing to do.
+int check_norm(NormRopeArgs& a, int dtype, bool backward) {
+  if (a.T < 0 || a.q_heads < 0 || a.k_heads < 0 || a.D < 1 || a.rotary < 0 || a.rotary % 2 != 0 || a.rotary > a.D ||
+      !rows_dtype_ok(dtype) || (a.layout != SV_ROPE_HALF && a.layout != SV_ROPE_INTERLEAVED) || !isfinite(a.mscale) ||
+      !norm_ok(a.norm.dtype, a.norm.eps))
+    return SV_ERR_INVALID_ARG;
+  if (a.D > SV_ATTN_MAX_HEAD_DIM || a.q_heads > SV_ATTN_MAX_HEADS || a.k_heads > SV_ATTN_MAX_HEADS ||
+      a.T > SV_ATTN_MAX_ROWS)
+    return SV_ERR_UNSUPPORTED;
+  if (a.q_heads == 0 && a.k_heads == 0) a.T = 0;
+  if (a.T == 0) return SV_OK;
+  if (a.rotary > 0 && (!a.freq || !a.positions)) return SV_ERR_INVALID_ARG;
+  auto rows_ok = [&](int heads, const RowsIn& x, const RowsIn& grad, const RowsOut& out) {
+    return heads == 0 || (x.p && out.p && read_strides_ok(x.token, x.head) &&
+                          write_strides_ok(a.T, heads, a.D, out.token, out.head) &&
+                          (!backward || (grad.p && read_strides_ok(grad.token, grad.head))));
+  };
+  return rows_ok(a.q_heads, a.q, a.dq, a.q_out) && rows_ok(a.k_heads, a.k, a.dk, a.k_out) ? SV_OK : SV_ERR_INVALID_ARG;
+}
+
+size_t norm_scratch(int T, int D) { return size_t(norm_parts(T)) * 2 * D * sizeof(float); }
+
 }  // namespace
 
 extern "C" {
@@ -161,40 +229,118 @@ int sv_kv_append(void* stream, int B, int T, int q_heads, int dtype, int rotary_
                  int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
                  int64_t v_head_stride, const int32_t* query_start, const int32_t* kv_len,
                  const sv_paged_cache* cache) {
-  int st = check_batch(B, T);
-  if (st != SV_OK) return st;
-  const bool empty = B == 0 || T == 0;
-  st = check_cache(cache, B, empty);
-  if (st != SV_OK) return st;
-  if (q_heads < 0 || !rows_dtype_ok(dtype) || rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > cache->head_dim ||
-      (layout != SV_ROPE_HALF && layout != SV_ROPE_INTERLEAVED) || !isfinite(mscale))
-    return SV_ERR_INVALID_ARG;
-  if (q_heads > SV_ATTN_MAX_HEADS) return SV_ERR_UNSUPPORTED;
-  if (empty) return SV_OK;
-  if (!k || !v || !query_start || !kv_len || (rotary_dim > 0 && !freq) || (q_heads > 0 && (!q || !q_out)))
-    return SV_ERR_INVALID_ARG;
-  if (!read_strides_ok(k_token_stride, k_head_stride) || !read_strides_ok(v_token_stride, v_head_stride))
-    return SV_ERR_INVALID_ARG;
-  if (q_heads > 0 && (!read_strides_ok(q_token_stride, q_head_stride) ||
-                      !write_strides_ok(T, q_heads, cache->head_dim, q_out_token_stride, q_out_head_stride)))
-    return SV_ERR_INVALID_ARG;
-  AppendArgs a;
-  a.B = B;
-  a.T = T;
-  a.q_heads = q_heads;
-  a.rotary = rotary_dim;
-  a.layout = layout;
-  a.freq = freq;
-  a.mscale = mscale;
-  a.positions = positions;
+  return append(stream, B, T, q_heads, dtype, rotary_dim, layout, freq, mscale, positions, nullptr,
+                {q, q_token_stride, q_head_stride}, {q_out, q_out_token_stride, q_out_head_stride},
+                {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, query_start, kv_len, cache);
+}
+
+int sv_kv_append_normed(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, int layout,
+                        const double* freq, float mscale, const int64_t* positions, int weight_dtype,
+                        const void* q_weight, const void* k_weight, float eps, const void* q, int64_t q_token_stride,
+                        int64_t q_head_stride, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                        const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                        int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,
+                        const int32_t* kv_len, const sv_paged_cache* cache) {
+  const NormWeights norm = {q_weight, k_weight, weight_dtype, eps};
+  return append(stream, B, T, q_heads, dtype, rotary_dim, layout, freq, mscale, positions, &norm,
+                {q, q_token_stride, q_head_stride}, {q_out, q_out_token_stride, q_out_head_stride},
+                {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, query_start, kv_len, cache);
+}
+
+int sv_qk_norm_rope(void* stream, int T, int q_heads, int k_heads, int head_dim, int rotary_dim, int layout, int dtype,
+                    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, int weight_dtype, const void* q_weight,
+                    const void* k_weight, float eps, const int64_t* positions, const double* freq, float mscale,
+                    void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                    int64_t k_out_token_stride, int64_t k_out_head_stride) {
+  NormRopeArgs a = {T, q_heads, k_heads, head_dim, rotary_dim, layout, {q_weight, k_weight, weight_dtype, eps}};
   a.q = {q, q_token_stride, q_head_stride};
   a.k = {k, k_token_stride, k_head_stride};
-  a.v = {v, v_token_stride, v_head_stride};
   a.q_out = {q_out, q_out_token_stride, q_out_head_stride};
-  a.query_start = query_start;
+  a.k_out = {k_out, k_out_token_stride, k_out_head_stride};
+  a.positions = positions;
+  a.freq = freq;
+  a.mscale = mscale;
+  const int st = check_norm(a, dtype, false);
+  if (st != SV_OK || a.T == 0) return st;
+  return to_status(launch_norm(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t sv_qk_norm_rope_backward_workspace_size(int T, int head_dim) {
+  if (T < 0 || T > SV_ATTN_MAX_ROWS || head_dim < 1 || head_dim > SV_ATTN_MAX_HEAD_DIM) return 0;
+  return 256 + norm_scratch(T, head_dim);
+}
+
+int sv_qk_norm_rope_backward(void* stream, int T, int q_heads, int k_heads, int head_dim, int rotary_dim, int layout,
+                             int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                             int64_t k_token_stride, int64_t k_head_stride, const void* dq_out,
+                             int64_t dq_out_token_stride, int64_t dq_out_head_stride, const void* dk_out,
+                             int64_t dk_out_token_stride, int64_t dk_out_head_stride, int weight_dtype,
+                             const void* q_weight, const void* k_weight, float eps, const int64_t* positions,
+                             const double* freq, float mscale, void* dq, int64_t dq_token_stride,
+                             int64_t dq_head_stride, void* dk, int64_t dk_token_stride, int64_t dk_head_stride,
+                             float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes) {
+  NormRopeArgs a = {T, q_heads, k_heads, head_dim, rotary_dim, layout, {q_weight, k_weight, weight_dtype, eps}};
+  a.q = {q, q_token_stride, q_head_stride};
+  a.k = {k, k_token_stride, k_head_stride};
+  a.dq = {dq_out, dq_out_token_stride, dq_out_head_stride};
+  a.dk = {dk_out, dk_out_token_stride, dk_out_head_stride};
+  a.q_out = {dq, dq_token_stride, dq_head_stride};
+  a.k_out = {dk, dk_token_stride, dk_head_stride};
+  a.positions = positions;
+  a.freq = freq;
+  a.mscale = mscale;
+  a.dq_weight = dq_weight;
+  a.dk_weight = dk_weight;
+  const int st = check_norm(a, dtype, true);
+  if (st != SV_OK) return st;
+  const bool weights = dq_weight || dk_weight;
+  if (a.T == 0 && !weights) return SV_OK;
+  if (weights && a.T > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < 256 + norm_scratch(T, head_dim)))
+    return SV_ERR_WORKSPACE;
+  a.part = weights ? static_cast<float*>(workspace) : nullptr;
+  return to_status(launch_norm_backward(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t sv_kv_pages_workspace_size(int B, int T) {
+  return check_batch(B, T) == SV_OK ? 256 + pages_scratch(B, T) : 0;
+}
+
+int sv_kv_pages(void* stream, int B, int T, int page_size, int max_pages, int num_pages, const int32_t* kv_len,
+                const int32_t* shared_pages, const int32_t* query_start, int32_t* page_table,
+                int64_t page_table_stride, int32_t* pages_held, int32_t* free_pages, int32_t* free_count,
+                int32_t* granted, int64_t* slots, int64_t* positions, void* workspace, size_t workspace_bytes) {
+  const int st = check_batch(B, T);
+  if (st != SV_OK) return st;
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0 || max_pages < 0 || num_pages < 0) return SV_ERR_INVALID_ARG;
+  if (page_size > SV_ATTN_MAX_PAGE || int64_t(max_pages) * page_size > SV_ATTN_MAX_TOKENS) return SV_ERR_UNSUPPORTED;
+  if (B == 0) return SV_OK;
+  if (!kv_len || !pages_held || !free_count || (max_pages > 0 && !page_table) || (num_pages > 0 && !free_pages) ||
+      (B > 1 && page_table_stride < max_pages) || page_table_stride < 0 || ((slots || positions) && T > 0 && !query_start))
+    return SV_ERR_INVALID_ARG;
+  if (!slots && !positions) query_start = nullptr;
+  if (pages_scratch(B, T) != 0 &&
+      (!workspace || !aligned16(workspace) || workspace_bytes < 256 + pages_scratch(B, T)))
+    return SV_ERR_WORKSPACE;
+  PagesArgs a;
+  a.B = B;
+  a.T = T;
+  a.page_shift = __builtin_ctz(unsigned(page_size));
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
   a.kv_len = kv_len;
-  a.cache = view_of(cache);
-  return to_status(launch_append(a, dtype, cache->dtype, static_cast<hipStream_t>(stream)));
+  a.shared = shared_pages;
+  a.query_start = T > 0 ? query_start : nullptr;
+  a.table = page_table;
+  a.table_stride = page_table_stride;
+  a.held = pages_held;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.granted = granted;
+  a.slots = slots;
+  a.positions = positions;
+  a.scratch = workspace;
+  return to_status(launch_pages(a, static_cast<hipStream_t>(stream)));
 }
 
 int sv_kv_gather(void* stream, int B, int T, int out_dtype, const sv_paged_cache* cache, const int32_t* row_start,

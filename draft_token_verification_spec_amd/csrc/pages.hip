@@ -1,0 +1,234 @@
+// Pages of a cache taken and given back as requests' lengths say, and the slots
+// of the new tokens.
+//
+// The free pages are a stack.  With need_b = ceil(kv_len[b] / page size) and
+// held_b pages of request b,
+//   give_b = max(held_b - need_b, 0),  take_b = max(need_b - held_b, 0),
+// the k-th page given back over all requests goes to place
+// count + sum(give) - 1 - k of the stack, and the k-th taken comes from place
+// C - 1 - k of the C = count + sum(give) pages then on it: exclusive sums over
+// the requests, and copies.  Taking right after is thus undone by giving back,
+// to the entry.
+//
+// Bound by latency: a scan and three dependent copies.  Up to 1024 requests
+// and kSmallRows rows one workgroup does it all, the copies shared evenly over
+// its threads, each of which finds its item's request by a search in LDS.
+// Otherwise three launches: the scan, the pages given back, and the pages taken
+// with the slots, the latter two by workgroups of one request each.
+#include "sv_attn.hpp"
+
+namespace sv {
+
+namespace {
+
+constexpr int kPagesThreads = 1024;
+constexpr int kMoveThreads = 256;
+
+struct Change {
+  int held, need;  // pages; need is not below the shared ones that are held
+  bool fits;       // the page table's row can hold `need` pages
+  __device__ __forceinline__ int give() const { return fits && held > need ? held - need : 0; }
+  __device__ __forceinline__ int take() const { return fits && need > held ? need - held : 0; }
+};
+
+__device__ __forceinline__ Change change_of(const PagesArgs& a, int b, int held) {
+  Change c;
+  c.held = min(max(held, 0), a.max_pages);
+  const int len = max(a.kv_len[b], 0);
+  c.need = int((int64_t(len) + (1 << a.page_shift) - 1) >> a.page_shift);
+  c.fits = c.need <= a.max_pages;
+  if (a.shared) c.need = max(c.need, min(a.shared[b], c.held));
+  return c;
+}
+
+__device__ __forceinline__ int64_t pages_on_stack(const PagesArgs& a) {
+  return min(max(*a.free_count, 0), a.num_pages);
+}
+
+// Exclusive sums over the workgroup of two numbers per thread; `total` gets the
+// sums.  Ends with every thread past its reads of `waves`.
+__device__ __forceinline__ longlong2 scan_pairs(longlong2 x, longlong2 (&waves)[kPagesThreads / 64], longlong2& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  longlong2 upto = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t p = __shfl_up(static_cast<long long>(upto.x), o, 64), q = __shfl_up(static_cast<long long>(upto.y), o, 64);
+    if (lane >= o) upto.x += p, upto.y += q;
+  }
+  if (lane == 63) waves[wave] = upto;
+  __syncthreads();
+  longlong2 before = {0, 0};
+  total = {0, 0};
+  for (int w = 0; w < kPagesThreads / 64; ++w) {
+    if (w < wave) before.x += waves[w].x, before.y += waves[w].y;
+    total.x += waves[w].x, total.y += waves[w].y;
+  }
+  __syncthreads();
+  return {before.x + upto.x - x.x, before.y + upto.y - x.y};
+}
+
+// The last of n ascending entries that is at most x (the first is).
+template <typename E, typename X>
+__device__ __forceinline__ int last_upto(const E* v, int n, X x) {
+  int lo = 0;
+  for (int step = 512; step > 0; step >>= 1)
+    if (lo + step < n && v[lo + step] <= x) lo += step;
+  return lo;
+}
+
+__device__ __forceinline__ void put_on_stack(const PagesArgs& a, int64_t at, int page) {
+  if (at >= 0 && at < a.num_pages) a.free_pages[at] = page;
+}
+
+// The slot of a row at `place` of a request that holds `held` pages, of which
+// those from `old` on are the taken-th and following ones taken of `count`.
+__device__ __forceinline__ void put_row(const PagesArgs& a, int t, int b, int64_t place, int held, int old, int64_t taken,
+                                        int64_t count) {
+  int64_t slot = -1;
+  const int64_t i = place >> a.page_shift;
+  if (place >= 0 && i < held) {
+    const int page = i < old ? a.table[b * a.table_stride + i] : a.free_pages[count - 1 - (taken + i - old)];
+    if (page >= 0 && page < a.num_pages) slot = (int64_t(page) << a.page_shift) + (place & ((1 << a.page_shift) - 1));
+  }
+  if (a.slots) a.slots[t] = slot;
+  if (a.positions) a.positions[t] = place;
+}
+
+__global__ __launch_bounds__(kPagesThreads) void pages_small_kernel(PagesArgs a) {
+  __shared__ longlong2 waves[kPagesThreads / 64];
+  __shared__ int64_t give_from[kPagesThreads], take_from[kPagesThreads];
+  __shared__ int old[kPagesThreads], now[kPagesThreads], start[kPagesThreads + 1], length[kPagesThreads];
+  const int b = threadIdx.x;
+  const bool live = b < a.B;
+  Change c = {0, 0, true};
+  if (live) {
+    c = change_of(a, b, a.held[b]);
+    length[b] = max(a.kv_len[b], 0);
+  }
+  if (a.query_start)
+    for (int i = b; i <= a.B; i += kPagesThreads) start[i] = a.query_start[i];
+  const int64_t count0 = pages_on_stack(a);
+  longlong2 total;
+  const longlong2 from = scan_pairs({c.give(), c.take()}, waves, total);
+  const int64_t count = min(count0 + total.x, int64_t(a.num_pages));
+  const int64_t upto = from.y + c.take();
+  const bool granted = c.fits && (c.take() == 0 || upto <= count);
+  if (live) {
+    give_from[b] = from.x, take_from[b] = from.y;
+    old[b] = c.held, now[b] = granted ? c.need : c.held;
+    if (a.granted) a.granted[b] = granted;
+    a.held[b] = now[b];
+  }
+  __syncthreads();  // (all have read the count)
+  const bool crosses = live && upto > count && from.y <= count;  // the first request that is refused
+  if (crosses || (b == a.B - 1 && upto <= count)) *a.free_count = int(count - (crosses ? from.y : upto));
+  for (int64_t k = b; k < total.x; k += kPagesThreads) {
+    const int r = last_upto(give_from, a.B, k);
+    int32_t* const entry = a.table + r * a.table_stride + now[r] + (k - give_from[r]);
+    put_on_stack(a, count0 + total.x - 1 - k, *entry);
+    *entry = -1;
+  }
+  __syncthreads();
+  for (int64_t k = b; k < min(total.y, count); k += kPagesThreads) {
+    const int r = last_upto(take_from, a.B, k);
+    const int i = int(k - take_from[r]);
+    if (i < now[r] - old[r]) a.table[r * a.table_stride + old[r] + i] = a.free_pages[count - 1 - k];
+  }
+  if (!a.query_start) return;
+  const int first = max(start[0], 0), end = min(start[a.B], a.T);
+  for (int t = first + b; t < end; t += kPagesThreads) {
+    const int r = last_upto(start, a.B, t);
+    if (t < start[r] || t >= start[r + 1]) continue;
+    put_row(a, t, r, int64_t(length[r]) - (int64_t(start[r + 1]) - t), now[r], old[r], take_from[r], count);
+  }
+}
+
+// What a scan leaves for the copies: [B] pairs of exclusive sums, the pages on
+// the stack before and after what is given back, [B] pages held before.
+__device__ __forceinline__ longlong2* sums_of(const PagesArgs& a) { return static_cast<longlong2*>(a.scratch) + 1; }
+__device__ __forceinline__ int32_t* held_of(const PagesArgs& a) { return reinterpret_cast<int32_t*>(sums_of(a) + a.B); }
+
+__global__ __launch_bounds__(kPagesThreads) void pages_scan_kernel(PagesArgs a) {
+  __shared__ longlong2 waves[kPagesThreads / 64];
+  longlong2 carry = {0, 0};
+  int held = int(threadIdx.x) < a.B ? a.held[threadIdx.x] : 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
+    const int b = b0 + threadIdx.x;
+    Change c = {0, 0, true};
+    if (b < a.B) c = change_of(a, b, held);
+    if (b + kPagesThreads < a.B) held = a.held[b + kPagesThreads];
+    longlong2 total;
+    const longlong2 from = scan_pairs({c.give(), c.take()}, waves, total);
+    if (b < a.B) {
+      sums_of(a)[b] = {carry.x + from.x, carry.y + from.y};
+      held_of(a)[b] = c.held;
+    }
+    carry.x += total.x, carry.y += total.y;
+  }
+  if (threadIdx.x == 0) {
+    const int64_t count = pages_on_stack(a);
+    *static_cast<longlong2*>(a.scratch) = {count + carry.x, min(count + carry.x, int64_t(a.num_pages))};
+  }
+}
+
+// Request blockIdx.x's pages that it gives back.
+__global__ __launch_bounds__(kMoveThreads) void pages_give_kernel(PagesArgs a) {
+  const int b = blockIdx.x;
+  const Change c = change_of(a, b, held_of(a)[b]);
+  const int64_t top = static_cast<longlong2*>(a.scratch)->x - 1 - sums_of(a)[b].x;
+  for (int i = blockIdx.y * kMoveThreads + threadIdx.x; i < c.give(); i += gridDim.y * kMoveThreads) {
+    int32_t* const entry = a.table + b * a.table_stride + c.need + i;
+    put_on_stack(a, top - i, *entry);
+    *entry = -1;
+  }
+}
+
+// Request blockIdx.x's pages that it takes, and its rows.
+__global__ __launch_bounds__(kMoveThreads) void pages_take_kernel(PagesArgs a) {
+  const int b = blockIdx.x, tid = blockIdx.y * kMoveThreads + threadIdx.x, all = gridDim.y * kMoveThreads;
+  const Change c = change_of(a, b, held_of(a)[b]);
+  const int64_t count = static_cast<longlong2*>(a.scratch)->y, from = sums_of(a)[b].y, upto = from + c.take();
+  const bool granted = c.fits && (c.take() == 0 || upto <= count);
+  const int now = granted ? c.need : c.held;
+  if (tid == 0) {
+    if (a.granted) a.granted[b] = granted;
+    a.held[b] = now;
+    const bool crosses = upto > count && from <= count;  // the first request that is refused
+    if (crosses || (b == a.B - 1 && upto <= count)) *a.free_count = int(count - (crosses ? from : upto));
+  }
+  for (int i = tid; i < now - c.held; i += all)
+    a.table[b * a.table_stride + c.held + i] = a.free_pages[count - 1 - (from + i)];
+  if (!a.query_start) return;
+  const int64_t start = a.query_start[b], end = a.query_start[b + 1], len = max(a.kv_len[b], 0);
+  for (int64_t t = max(start, int64_t(0)) + tid; t < min(end, int64_t(a.T)); t += all)
+    put_row(a, int(t), b, len - (end - t), now, c.held, from, count);
+}
+
+// Rows that one workgroup takes along.
+constexpr int kSmallRows = 8192;
+
+bool small(int B, int T) { return B <= kPagesThreads && T <= kSmallRows; }
+
+}  // namespace
+
+size_t pages_scratch(int B, int T) {
+  return small(B, T) ? 0 : sizeof(longlong2) * (size_t(B) + 1) + sizeof(int32_t) * size_t(B);
+}
+
+hipError_t launch_pages(const PagesArgs& a, hipStream_t stream) {
+  if (small(a.B, a.T)) {
+    hipLaunchKernelGGL(pages_small_kernel, dim3(1), dim3(kPagesThreads), 0, stream, a);
+    return hipGetLastError();
+  }
+  // workgroups for few requests of many rows: four for a compute unit
+  int per = (1024 + a.B - 1) / a.B;
+  const int rows = (a.T + a.B - 1) / a.B, most = (rows + kMoveThreads - 1) / kMoveThreads;
+  per = per < most ? per : most;
+  const dim3 grid(a.B, per < 1 ? 1 : per);
+  hipLaunchKernelGGL(pages_scan_kernel, dim3(1), dim3(kPagesThreads), 0, stream, a);
+  hipLaunchKernelGGL(pages_give_kernel, dim3(a.B, 1), dim3(kMoveThreads), 0, stream, a);
+  hipLaunchKernelGGL(pages_take_kernel, grid, dim3(kMoveThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace sv

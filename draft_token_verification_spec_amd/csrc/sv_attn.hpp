@@ -27,6 +27,34 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a, int dtype, hipStream_t stream);
 
+// Norms of query and key heads: weights of head_dim channels (null: ones).
+struct NormWeights {
+  const void* q;
+  const void* k;
+  int dtype;
+  float eps;
+};
+
+// Queries and keys [T, heads, D] normed and turned, or (launch_norm_backward)
+// the gradients of that: dq, dk with respect to its outputs come in, q_out,
+// k_out with respect to q, k and the weights' go out.
+struct NormRopeArgs {
+  int T, q_heads, k_heads, D, rotary;
+  int layout;
+  NormWeights norm;
+  RowsIn q, k, dq, dk;
+  RowsOut q_out, k_out;
+  const int64_t* positions;
+  const double* freq;
+  float mscale;
+  float* part;        // [norm_parts(T)][2][D], the weights' gradients of a workgroup's rows
+  float* dq_weight;   // nullable
+  float* dk_weight;   // nullable
+};
+int norm_parts(int T);  // workgroups of the backward pass
+hipError_t launch_norm(const NormRopeArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_norm_backward(const NormRopeArgs& a, int dtype, hipStream_t stream);
+
 struct AppendArgs {
   int B, T, q_heads, rotary;
   int layout;
@@ -38,8 +66,30 @@ struct AppendArgs {
   const int32_t* query_start;
   const int32_t* kv_len;
   PagedView cache;
+  bool normed;
+  NormWeights norm;
 };
 hipError_t launch_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
+
+// Pages taken and given back.  scratch: pages_scratch(B, T) bytes (0: none).
+struct PagesArgs {
+  int B, T;
+  int page_shift, max_pages, num_pages;
+  const int32_t* kv_len;
+  const int32_t* shared;       // nullable
+  const int32_t* query_start;  // nullable: no rows
+  int32_t* table;
+  int64_t table_stride;
+  int32_t* held;
+  int32_t* free_pages;
+  int32_t* free_count;
+  int32_t* granted;    // nullable
+  int64_t* slots;      // nullable
+  int64_t* positions;  // nullable
+  void* scratch;
+};
+size_t pages_scratch(int B, int T);
+hipError_t launch_pages(const PagesArgs& a, hipStream_t stream);
 
 struct GatherArgs {
   int B, T;

@@ -155,6 +155,106 @@ int sv_kv_append(void* stream, int B, int T, int q_heads, int dtype, int rotary_
                  int64_t v_head_stride, const int32_t* query_start, const int32_t* kv_len,
                  const sv_paged_cache* cache);
 
+/* Norms of query and key heads with their rotary positions in one pass: each
+ * head's row x becomes rope(x * r * w), r = (mean of x^2 over head_dim +
+ * eps)^-1/2, w the weights of queries or of keys, rope as by sv_rope (which
+ * says what layouts, strides and positions may be).
+ *   q, k, q_out, k_out   SV_F32 or SV_BF16 (dtype), [T, q_heads or k_heads,
+ *              head_dim] with the given strides; an output may be its input
+ *              with the same strides, else none may overlap another array.
+ *              Heads 0: there are no queries, or no keys.
+ *   q_weight, k_weight   [head_dim], SV_F32 or SV_BF16 (weight_dtype); NULL:
+ *              all 1.
+ *   eps        > 0, finite.
+ *   positions  int64 [T]; not read with rotary_dim 0.
+ * The sum of squares and all products are binary32, the result is rounded once:
+ * a row whose sum of squares passes 3.4e38 has no meaningful result. */
+int sv_qk_norm_rope(void* stream, int T, int q_heads, int k_heads, int head_dim, int rotary_dim, int layout, int dtype,
+                    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, int weight_dtype, const void* q_weight,
+                    const void* k_weight, float eps, const int64_t* positions, const double* freq, float mscale,
+                    void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                    int64_t k_out_token_stride, int64_t k_out_head_stride);
+
+/* Bytes of workspace that sv_qk_norm_rope_backward needs where a weight's
+ * gradient is asked for; 0 for sizes that the call would reject. */
+size_t sv_qk_norm_rope_backward_workspace_size(int T, int head_dim);
+
+/* The gradients of sv_qk_norm_rope: from dq_out, dk_out (with respect to its
+ * outputs; type and shape as q, k) those with respect to q, k and the weights.
+ *   dq, dk     as q, k; each may be its dq_out or q (dk_out or k) with the same
+ *              strides.
+ *   dq_weight, dk_weight   float [head_dim] (also where the weights themselves
+ *              are NULL), or NULL: not asked for.  Sums over rows and heads in
+ *              binary32, in an order that depends on T alone; 0 with T == 0.
+ *   workspace  scratch of this call alone, 16-byte aligned; NULL where neither
+ *              weight's gradient is asked for. */
+int sv_qk_norm_rope_backward(void* stream, int T, int q_heads, int k_heads, int head_dim, int rotary_dim, int layout,
+                             int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                             int64_t k_token_stride, int64_t k_head_stride, const void* dq_out,
+                             int64_t dq_out_token_stride, int64_t dq_out_head_stride, const void* dk_out,
+                             int64_t dk_out_token_stride, int64_t dk_out_head_stride, int weight_dtype,
+                             const void* q_weight, const void* k_weight, float eps, const int64_t* positions,
+                             const double* freq, float mscale, void* dq, int64_t dq_token_stride,
+                             int64_t dq_head_stride, void* dk, int64_t dk_token_stride, int64_t dk_head_stride,
+                             float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes);
+
+/* sv_kv_append with norms: keys and queries are normed as by sv_qk_norm_rope
+ * before they are turned, in binary32 with one rounding at the end; values are
+ * not normed. */
+int sv_kv_append_normed(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, int layout,
+                        const double* freq, float mscale, const int64_t* positions, int weight_dtype,
+                        const void* q_weight, const void* k_weight, float eps, const void* q, int64_t q_token_stride,
+                        int64_t q_head_stride, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                        const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                        int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,
+                        const int32_t* kv_len, const sv_paged_cache* cache);
+
+/* Bytes of workspace that sv_kv_pages needs; 256 stands for none (the call then
+ * takes a NULL workspace), 0 for sizes that the call would reject. */
+size_t sv_kv_pages_workspace_size(int B, int T);
+
+/* Pages of a cache for B requests: after the call request b holds the
+ * ceil(kv_len[b] / page_size) pages that its length needs (a negative length
+ * counts as 0), as the first entries of its page table's row.  All in place:
+ *   page_table int32 [B, max_pages] with page_table_stride >= max_pages
+ *              entries between rows.  Entries of pages given back become -1;
+ *              those from pages_held[b] on are not read: initialise them to -1,
+ *              so that no call sees tokens there.
+ *   pages_held int32 [B], the pages that each request holds (counted as within
+ *              0..max_pages).
+ *   free_pages int32 [num_pages], free_count int32 [1]: the free pages are the
+ *              first free_count[0] entries, a stack whose top is the last of
+ *              them.
+ *   shared_pages   int32 [B] or NULL (0): so many of the first pages that a
+ *              request holds are not given back (others hold them too).
+ * First pages are given back: the k-th of all (requests in order, a request's
+ * pages in the order of its row) becomes the k-th from the top of the stack.
+ * Then pages are taken: requests in order, each page from the top.  A request is
+ * granted its pages if the stack has enough for all that the requests before it
+ * and it itself lack; from the first that is not granted on, none is that lacks
+ * a page, and what it holds stays as it was.  Nor is one that needs more than
+ * max_pages.  Taking pages and giving the same ones back leaves the stack as it
+ * was.
+ *   granted    int32 [B] or NULL: 1 if the request holds what its length needs.
+ *   query_start    int32 [B + 1] or NULL: packed new tokens, of which
+ *   slots      int64 [T] or NULL gets page * page_size + place % page_size of
+ *              each row's place, -1 where the request holds no page for it or
+ *              the page is outside 0..num_pages-1, and
+ *   positions  int64 [T] or NULL the place (as sv_rope and sv_qk_norm_rope take
+ *              it); rows of no request are left as they were.
+ *   page_size  a power of two up to SV_ATTN_MAX_PAGE.  num_pages, the pages of
+ *              the cache, below 2^31; max_pages * page_size at most
+ *              SV_ATTN_MAX_TOKENS.
+ *   workspace  scratch of this call alone, 16-byte aligned.
+ * A page should be held by one request only, but for shared ones, and not be
+ * free as well; where it is not so no memory beyond the arrays is touched (what
+ * is given back beyond num_pages entries is dropped). */
+int sv_kv_pages(void* stream, int B, int T, int page_size, int max_pages, int num_pages, const int32_t* kv_len,
+                const int32_t* shared_pages, const int32_t* query_start, int32_t* page_table,
+                int64_t page_table_stride, int32_t* pages_held, int32_t* free_pages, int32_t* free_count,
+                int32_t* granted, int64_t* slots, int64_t* positions, void* workspace, size_t workspace_bytes);
+
 /* Reads tokens of a paged cache back into contiguous rows: row
  * row_start[b] + i of k_out and v_out, i < row_start[b+1] - row_start[b], gets
  * the token at place kv_begin[b] + i of request b (kv_begin NULL: 0), as the
