@@ -41,6 +41,10 @@ __all__ = [
     "sv_kv_gather",
     "sv_paged_attention",
     "sv_paged_attention_workspace_size",
+    "sv_paged_attention_sinks",
+    "sv_paged_attention_sinks_workspace_size",
+    "sv_paged_attention_shared",
+    "sv_paged_attention_shared_workspace_size",
 ]
 
 SV_E4M3 = 2
@@ -79,6 +83,12 @@ _SIGNATURES = {
     "sv_paged_attention_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "sv_paged_attention": (_i, [_p, _i, _i, _i, _p, _i64, _i64, _p, _p, _p, _i, _i, _f, _i, _p, _i64, _i64, _p, _p,
                                 _sz]),
+    "sv_paged_attention_sinks_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "sv_paged_attention_sinks": (_i, [_p, _i, _i, _i, _p, _i64, _i64, _p, _p, _p, _i, _i, _f, _i, _i, _p, _i64, _i64, _p,
+                                      _p, _sz]),
+    "sv_paged_attention_shared_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "sv_paged_attention_shared": (_i, [_p, _i, _i, _i, _p, _i64, _i64, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _f, _p,
+                                       _i64, _i64, _p, _p, _sz]),
 }
 
 _lib = None
@@ -584,6 +594,35 @@ def sv_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     return o
 
 
+def _attention_call(q, k_cache, v_cache, page_table, query_start, kv_len, k_scale, v_scale, want_lse, out):
+    """What the attention calls have in common: (device, (B, T, q_heads, kv heads, D), page table's tokens, the arguments up
+    to kv_len, those from out to lse, the outputs)."""
+    dev = _tensor("q", q)
+    shape = T, q_heads, D = _three("q", q)
+    _tensor("kv_len", kv_len)
+    B = kv_len.numel()
+    cache, heads, cache_dim, tokens = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
+    if cache_dim != D:
+        raise ValueError(f"q is {list(shape)}, the cache has heads of {cache_dim} channels")
+    qr = _rows(dev, "q", q, torch.bfloat16, shape)
+    qs = _array(dev, "query_start", query_start, torch.int32, (B + 1,))
+    kl = _array(dev, "kv_len", kv_len, torch.int32, (B,))
+    o = {} if out is None else out
+    device = q.device
+    if "out" in o:
+        orows = _rows(dev, "out['out']", o["out"], torch.bfloat16, shape)
+    else:
+        t = o["out"] = _new(shape, torch.bfloat16, device)
+        orows = t.data_ptr(), q_heads * D, D
+    lse = None
+    if "lse" in o:
+        lse = _array(dev, "out['lse']", o["lse"], torch.float32, (T, q_heads))
+    elif want_lse:
+        t = o["lse"] = torch.empty_strided((T, q_heads), (q_heads, 1), dtype=torch.float32, device=device)
+        lse = t.data_ptr()
+    return dev, (B, T, q_heads, heads, D), tokens, (B, T, q_heads, *qr, cache, qs, kl), (*orows, lse), o
+
+
 @functools.lru_cache(maxsize=4096)
 def sv_paged_attention_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int = 0,
                                       max_kv_len: int = 0) -> int:
@@ -613,40 +652,81 @@ def sv_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     own duration: calls on different streams, and captured graphs, then share
     nothing.  Else a contiguous uint8 tensor of at least
     ``sv_paged_attention_workspace_size`` bytes, used by one call at a time."""
-    dev = _tensor("q", q)
-    shape = T, q_heads, D = _three("q", q)
-    _tensor("kv_len", kv_len)
-    B = kv_len.numel()
-    cache, heads, cache_dim, tokens = _paged(dev, B, k_cache, v_cache, page_table, k_scale, v_scale)
-    if cache_dim != D:
-        raise ValueError(f"q is {list(shape)}, the cache has heads of {cache_dim} channels")
-    qr = _rows(dev, "q", q, torch.bfloat16, shape)
-    qs = _array(dev, "query_start", query_start, torch.int32, (B + 1,))
-    kl = _array(dev, "kv_len", kv_len, torch.int32, (B,))
-    o = {} if out is None else out
-    device = q.device
-    if "out" in o:
-        orows = _rows(dev, "out['out']", o["out"], torch.bfloat16, shape)
-    else:
-        t = o["out"] = _new(shape, torch.bfloat16, device)
-        orows = t.data_ptr(), q_heads * D, D
-    lse = None
-    if "lse" in o:
-        lse = _array(dev, "out['lse']", o["lse"], torch.float32, (T, q_heads))
-    elif want_lse:
-        t = o["lse"] = torch.empty_strided((T, q_heads), (q_heads, 1), dtype=torch.float32, device=device)
-        lse = t.data_ptr()
+    dev, sizes, tokens, args, results, o = _attention_call(q, k_cache, v_cache, page_table, query_start, kv_len, k_scale,
+                                                           v_scale, want_lse, out)
     if max_kv_len == 0:
         max_kv_len = tokens
-    nbytes = sv_paged_attention_workspace_size(B, T, q_heads, heads, D, max_q_len, max_kv_len)
-    ws = None
-    if workspace is None:
-        if nbytes > 256:
-            ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
-    else:
-        ws = workspace
-        _array(dev, "workspace", ws, torch.uint8, (ws.numel(),))
-        nbytes = ws.numel()
-    _call(dev, "sv_paged_attention", B, T, q_heads, *qr, cache, qs, kl, _wide(max_q_len), _wide(max_kv_len),
-          D ** -0.5 if scale is None else scale, _wide(window), *orows, lse, None if ws is None else ws.data_ptr(), nbytes)
+    ws, nbytes = _scratch(dev, sv_paged_attention_workspace_size(*sizes, max_q_len, max_kv_len), workspace, q.device)
+    _call(dev, "sv_paged_attention", *args, _wide(max_q_len), _wide(max_kv_len), sizes[4] ** -0.5 if scale is None else scale,
+          _wide(window), *results, None if ws is None else ws.data_ptr(), nbytes)
+    return o
+
+
+@functools.lru_cache(maxsize=4096)
+def sv_paged_attention_sinks_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int = 0,
+                                            max_kv_len: int = 0, window: int = 0, sinks: int = 0) -> int:
+    return int(_attn_lib().sv_paged_attention_sinks_workspace_size(B, T, q_heads, kv_heads, head_dim, _wide(max_q_len),
+                                                                   _wide(max_kv_len), _wide(window), _wide(sinks)))
+
+
+def sv_paged_attention_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                             query_start: torch.Tensor, kv_len: torch.Tensor, *, window: int, sinks: int,
+                             scale: Optional[float] = None, k_scale: Optional[torch.Tensor] = None,
+                             v_scale: Optional[torch.Tensor] = None, max_q_len: int = 0, max_kv_len: int = 0,
+                             want_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                             out: Optional[dict] = None) -> dict:
+    """``sv_paged_attention`` where a row sees, beside the last ``window`` tokens
+    up to its own, the first ``sinks`` of its request; see
+    ``sv_paged_attention_sinks``.  All else as there; a ``workspace`` has
+    ``sv_paged_attention_sinks_workspace_size`` bytes."""
+    dev, sizes, tokens, args, results, o = _attention_call(q, k_cache, v_cache, page_table, query_start, kv_len, k_scale,
+                                                           v_scale, want_lse, out)
+    if max_kv_len == 0:
+        max_kv_len = tokens
+    nbytes = sv_paged_attention_sinks_workspace_size(*sizes, max_q_len, max_kv_len, window, sinks)
+    ws, nbytes = _scratch(dev, nbytes, workspace, q.device)
+    _call(dev, "sv_paged_attention_sinks", *args, _wide(max_q_len), _wide(max_kv_len),
+          sizes[4] ** -0.5 if scale is None else scale, _wide(window), _wide(sinks), *results,
+          None if ws is None else ws.data_ptr(), nbytes)
+    return o
+
+
+@functools.lru_cache(maxsize=4096)
+def sv_paged_attention_shared_workspace_size(B: int, T: int, groups: int, q_heads: int, kv_heads: int, head_dim: int,
+                                             max_q_len: int = 0, max_group_len: int = 0, max_shared_len: int = 0,
+                                             max_own_len: int = 0) -> int:
+    return int(_attn_lib().sv_paged_attention_shared_workspace_size(
+        B, T, groups, q_heads, kv_heads, head_dim, _wide(max_q_len), _wide(max_group_len), _wide(max_shared_len),
+        _wide(max_own_len)))
+
+
+def sv_paged_attention_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                              query_start: torch.Tensor, kv_len: torch.Tensor, group_start: torch.Tensor,
+                              shared_len: torch.Tensor, *, scale: Optional[float] = None,
+                              k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                              max_q_len: int = 0, max_group_len: int = 0, max_shared_len: int = 0, max_own_len: int = 0,
+                              want_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                              out: Optional[dict] = None) -> dict:
+    """``sv_paged_attention`` for requests whose first tokens are the same, which
+    are read once for all of them; see ``sv_paged_attention_shared``.
+    ``group_start`` int32 [groups + 1] (requests of a group follow each other),
+    ``shared_len`` int32 [groups]; the group's first request's row of the page
+    table holds the shared pages.
+
+    ``max_q_len``, ``max_group_len``, ``max_shared_len``, ``max_own_len``: the
+    most new tokens of a request and of a group, the most shared tokens, the most
+    tokens of a request that are not shared, where known (the last two default to
+    the page table's width).  They change times, not results.  A ``workspace`` has
+    ``sv_paged_attention_shared_workspace_size`` bytes."""
+    dev, sizes, tokens, args, results, o = _attention_call(q, k_cache, v_cache, page_table, query_start, kv_len, k_scale,
+                                                           v_scale, want_lse, out)
+    _tensor("shared_len", shared_len)
+    groups = shared_len.numel()
+    gs = _array(dev, "group_start", group_start, torch.int32, (groups + 1,))
+    sl = _array(dev, "shared_len", shared_len, torch.int32, (groups,))
+    hints = max_q_len, max_group_len, max_shared_len or tokens, max_own_len or tokens
+    nbytes = sv_paged_attention_shared_workspace_size(sizes[0], sizes[1], groups, *sizes[2:], *hints)
+    ws, nbytes = _scratch(dev, nbytes, workspace, q.device)
+    _call(dev, "sv_paged_attention_shared", *args, groups, gs, sl, *(_wide(h) for h in hints),
+          sizes[4] ** -0.5 if scale is None else scale, *results, None if ws is None else ws.data_ptr(), nbytes)
     return o

@@ -158,6 +158,68 @@ int check_norm(NormRopeArgs& a, int dtype, bool backward) {
 
 size_t norm_scratch(int T, int D) { return size_t(norm_parts(T)) * 2 * D * sizeof(float); }
 
+// Checks of an attention call, and its arguments where there is something to do
+// (a.T is 0 otherwise).  The plan and the parts are the caller's part.
+int check_attention(AttnArgs& a, int B, int T, int q_heads, const RowsIn& q, const sv_paged_cache* cache,
+                    const int32_t* query_start, const int32_t* kv_len, int max_q_len, int max_kv_len, float scale,
+                    int window, const RowsOut& out, float* lse) {
+  a.T = 0;
+  int st = check_batch(B, T);
+  if (st != SV_OK) return st;
+  const bool empty = B == 0 || T == 0;
+  st = check_cache(cache, B, empty);
+  if (st != SV_OK) return st;
+  st = check_attention_sizes(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
+  if (st != SV_OK) return st;
+  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f) || window < 0) return SV_ERR_INVALID_ARG;
+  if (empty) return SV_OK;
+  if (!q.p || !out.p || !query_start || !kv_len || !aligned16(q.p) || !aligned16(out.p)) return SV_ERR_INVALID_ARG;
+  for (int64_t s : {q.token, out.token})
+    if (s < 0 || (T > 1 && s % 8 != 0)) return SV_ERR_INVALID_ARG;
+  for (int64_t s : {q.head, out.head})
+    if (s < 0 || (q_heads > 1 && s % 8 != 0)) return SV_ERR_INVALID_ARG;
+  if (!write_strides_ok(T, q_heads, cache->head_dim, out.token, out.head)) return SV_ERR_INVALID_ARG;
+  a.B = B;
+  a.T = T;
+  a.q_heads = q_heads;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.query_start = query_start;
+  a.kv_len = kv_len;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = 0;
+  a.groups = 0;
+  a.group_start = a.shared_len = nullptr;
+  const PagedView v = view_of(cache);
+  const int shift = cache->dtype == SV_BF16 ? 3 : 4;  // elements of 16 bytes
+  a.cache.table = v.table;
+  a.cache.table_stride = v.table_stride;
+  a.cache.k = v.k;
+  a.cache.v = v.v;
+  a.cache.k_scale = v.k_scale;
+  a.cache.v_scale = v.v_scale;
+  a.cache.ku = {uint32_t(v.k_page >> shift), uint32_t(v.k_token >> shift), uint32_t(v.k_head >> shift)};
+  a.cache.vu = {uint32_t(v.v_page >> shift), uint32_t(v.v_token >> shift), uint32_t(v.v_head >> shift)};
+  a.cache.max_pages = v.max_pages;
+  a.cache.num_pages = v.num_pages;
+  a.cache.heads = v.heads;
+  a.cache.D = v.D;
+  a.cache.page_shift = v.page_shift;
+  return SV_OK;
+}
+
+bool scratch_ok(const void* workspace, size_t have, size_t need) {
+  return need == 0 || (workspace && aligned16(workspace) && have >= 256 + need);
+}
+
+// A plan's parts in the workspace.
+void place_parts(AttnPlan& p, void* workspace) {
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
+}
+
 }  // namespace
 
 extern "C" {
@@ -376,54 +438,79 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
                        const int32_t* kv_len, int max_q_len, int max_kv_len, float scale, int window, void* out,
                        int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
                        size_t workspace_bytes) {
-  int st = check_batch(B, T);
-  if (st != SV_OK) return st;
-  const bool empty = B == 0 || T == 0;
-  st = check_cache(cache, B, empty);
-  if (st != SV_OK) return st;
-  st = check_attention_sizes(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
-  if (st != SV_OK) return st;
-  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f) || window < 0) return SV_ERR_INVALID_ARG;
-  if (empty) return SV_OK;
-  if (!q || !out || !query_start || !kv_len || !aligned16(q) || !aligned16(out)) return SV_ERR_INVALID_ARG;
-  for (int64_t s : {q_token_stride, out_token_stride})
-    if (s < 0 || (T > 1 && s % 8 != 0)) return SV_ERR_INVALID_ARG;
-  for (int64_t s : {q_head_stride, out_head_stride})
-    if (s < 0 || (q_heads > 1 && s % 8 != 0)) return SV_ERR_INVALID_ARG;
-  if (!write_strides_ok(T, q_heads, cache->head_dim, out_token_stride, out_head_stride)) return SV_ERR_INVALID_ARG;
-  AttnPlan p = plan_attention(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
-  if (p.num_splits > 1 &&
-      (!workspace || !aligned16(workspace) || workspace_bytes < 256 + p.ml_bytes + p.o_bytes))
-    return SV_ERR_WORKSPACE;
-  p.part_ml = static_cast<float2*>(workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
   AttnArgs a;
-  a.B = B;
-  a.T = T;
-  a.q_heads = q_heads;
-  a.q = {q, q_token_stride, q_head_stride};
-  a.out = {out, out_token_stride, out_head_stride};
-  a.lse = lse;
-  a.query_start = query_start;
-  a.kv_len = kv_len;
-  a.scale = scale;
-  a.window = window;
-  const PagedView v = view_of(cache);
-  const int shift = cache->dtype == SV_BF16 ? 3 : 4;  // elements of 16 bytes
-  a.cache.table = v.table;
-  a.cache.table_stride = v.table_stride;
-  a.cache.k = v.k;
-  a.cache.v = v.v;
-  a.cache.k_scale = v.k_scale;
-  a.cache.v_scale = v.v_scale;
-  a.cache.ku = {uint32_t(v.k_page >> shift), uint32_t(v.k_token >> shift), uint32_t(v.k_head >> shift)};
-  a.cache.vu = {uint32_t(v.v_page >> shift), uint32_t(v.v_token >> shift), uint32_t(v.v_head >> shift)};
-  a.cache.max_pages = v.max_pages;
-  a.cache.num_pages = v.num_pages;
-  a.cache.heads = v.heads;
-  a.cache.D = v.D;
-  a.cache.page_shift = v.page_shift;
+  const int st = check_attention(a, B, T, q_heads, {q, q_token_stride, q_head_stride}, cache, query_start, kv_len,
+                                 max_q_len, max_kv_len, scale, window, {out, out_token_stride, out_head_stride}, lse);
+  if (st != SV_OK || a.T == 0) return st;
+  AttnPlan p = plan_attention(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len);
+  if (!scratch_ok(workspace, workspace_bytes, p.ml_bytes + p.o_bytes)) return SV_ERR_WORKSPACE;
+  place_parts(p, workspace);
   return to_status(launch_attention(a, p, cache->dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t sv_paged_attention_sinks_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim, int max_q_len,
+                                               int max_kv_len, int window, int sinks) {
+  if (check_attention_sizes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len) != SV_OK || window < 0 || sinks < 0)
+    return 0;
+  const AttnPlan p = plan_sinks(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len, window, sinks);
+  return 256 + p.ml_bytes + p.o_bytes;
+}
+
+int sv_paged_attention_sinks(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
+                             int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
+                             const int32_t* kv_len, int max_q_len, int max_kv_len, float scale, int window, int sinks,
+                             void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
+                             size_t workspace_bytes) {
+  AttnArgs a;
+  const int st = check_attention(a, B, T, q_heads, {q, q_token_stride, q_head_stride}, cache, query_start, kv_len,
+                                 max_q_len, max_kv_len, scale, window, {out, out_token_stride, out_head_stride}, lse);
+  if (st != SV_OK) return st;
+  if (sinks < 0) return SV_ERR_INVALID_ARG;
+  if (a.T == 0) return SV_OK;
+  a.sinks = sinks;
+  AttnPlan p = plan_sinks(B, T, q_heads, cache->heads, cache->head_dim, max_q_len, max_kv_len, window, sinks);
+  if (!scratch_ok(workspace, workspace_bytes, p.ml_bytes + p.o_bytes)) return SV_ERR_WORKSPACE;
+  place_parts(p, workspace);
+  return to_status(launch_sinks(a, p, cache->dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t sv_paged_attention_shared_workspace_size(int B, int T, int groups, int q_heads, int kv_heads, int head_dim,
+                                                int max_q_len, int max_group_len, int max_shared_len, int max_own_len) {
+  if (check_attention_sizes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_own_len) != SV_OK || groups < 0 ||
+      groups > SV_MAX_B || max_group_len < 0 || max_shared_len < 0)
+    return 0;
+  if (groups == 0) return sv_paged_attention_workspace_size(B, T, q_heads, kv_heads, head_dim, max_q_len, max_own_len);
+  return 256 + plan_shared(B, T, groups, q_heads, kv_heads, head_dim, max_q_len, max_group_len, max_shared_len,
+                           max_own_len).bytes;
+}
+
+int sv_paged_attention_shared(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
+                              const int32_t* kv_len, int groups, const int32_t* group_start, const int32_t* shared_len,
+                              int max_q_len, int max_group_len, int max_shared_len, int max_own_len, float scale,
+                              void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
+                              size_t workspace_bytes) {
+  if (groups == 0)  // nothing is shared
+    return sv_paged_attention(stream, B, T, q_heads, q, q_token_stride, q_head_stride, cache, query_start, kv_len,
+                              max_q_len, max_own_len, scale, 0, out, out_token_stride, out_head_stride, lse, workspace,
+                              workspace_bytes);
+  AttnArgs a;
+  const int st = check_attention(a, B, T, q_heads, {q, q_token_stride, q_head_stride}, cache, query_start, kv_len,
+                                 max_q_len, max_own_len, scale, 0, {out, out_token_stride, out_head_stride}, lse);
+  if (st != SV_OK) return st;
+  if (groups < 0 || max_group_len < 0 || max_shared_len < 0) return SV_ERR_INVALID_ARG;
+  if (groups > SV_MAX_B) return SV_ERR_UNSUPPORTED;
+  if (a.T == 0) return SV_OK;
+  if (!group_start || !shared_len) return SV_ERR_INVALID_ARG;
+  a.groups = groups;
+  a.group_start = group_start;
+  a.shared_len = shared_len;
+  SharedPlan p = plan_shared(B, T, groups, q_heads, cache->heads, cache->head_dim, max_q_len, max_group_len,
+                             max_shared_len, max_own_len);
+  if (!scratch_ok(workspace, workspace_bytes, p.bytes)) return SV_ERR_WORKSPACE;
+  place_parts(p.shared, workspace);
+  place_parts(p.own, workspace);
+  return to_status(launch_shared(a, p, cache->dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,24 @@
+// Attention over a paged cache with a sliding window and a few first tokens that
+// stay visible: the kernels of sv_attn_kernels.hpp over a range of tokens with a
+// gap between the two.
+#include "sv_attn_kernels.hpp"
+
+namespace sv {
+
+// A tile of rows reads the first tokens, its window's and its own rows' at most:
+// contexts are divided as if they were no longer than that (and the pieces of
+// tokens that the ends of the two lie in).
+AttnPlan plan_sinks(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len, int window, int sinks) {
+  const AttnPlan p = plan_attention(B, T, q_heads, kv_heads, D, max_q_len, max_kv_len);
+  if (window == 0) return p;
+  const int64_t reach = int64_t(window) + sinks + p.row_tile / (q_heads / kv_heads) + 2 * kTile;
+  return reach < max_kv_len ? plan_attention(B, T, q_heads, kv_heads, D, max_q_len, int(reach)) : p;
+}
+
+hipError_t launch_sinks(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream) {
+  if (a.window == 0) return launch_attention(a, p, cache_dtype, stream);  // every row sees all before it
+  launch_part<Part::kSinks>(a, p, cache_dtype, stream);
+  return hipGetLastError();
+}
+
+}  // namespace sv

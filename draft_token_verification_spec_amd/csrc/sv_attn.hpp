@@ -128,6 +128,10 @@ struct AttnArgs {
   float scale;
   int window;  // 0: none
   CacheView cache;
+  int sinks;   // first tokens seen beside the window
+  int groups;  // of requests that share their first tokens
+  const int32_t* group_start;
+  const int32_t* shared_len;
 };
 
 // How a call is divided: row_tile rows a workgroup, `tiles` workgroups for a
@@ -136,11 +140,26 @@ struct AttnArgs {
 // and row t, head h are at (s * T + t) * q_heads + h.
 struct AttnPlan {
   int row_tile, tiles, split_len, num_splits;
+  int first_part;   // of the call's splits, where several kernels' parts are joined
   size_t ml_bytes, o_bytes;
   float2* part_ml;  // maximum (base-2 logarithm), sum of weights
   float* part_o;    // weighted values
 };
 AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream);
+
+// With a window and first tokens that stay visible.
+AttnPlan plan_sinks(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len, int window, int sinks);
+hipError_t launch_sinks(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream);
+
+// Behind tokens that groups of requests share: how those are divided, and each
+// request's own, whose parts follow.
+struct SharedPlan {
+  AttnPlan shared, own;
+  size_t bytes;
+};
+SharedPlan plan_shared(int B, int T, int groups, int q_heads, int kv_heads, int D, int max_q_len, int max_group_len,
+                       int max_shared_len, int max_own_len);
+hipError_t launch_shared(const AttnArgs& a, const SharedPlan& p, int cache_dtype, hipStream_t stream);
 
 }  // namespace sv

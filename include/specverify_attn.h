@@ -316,6 +316,53 @@ int sv_paged_attention(void* stream, int B, int T, int q_heads, const void* q, i
                        int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
                        size_t workspace_bytes);
 
+/* Bytes of workspace that sv_paged_attention_sinks needs, as
+ * sv_paged_attention_workspace_size. */
+size_t sv_paged_attention_sinks_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim, int max_q_len,
+                                               int max_kv_len, int window, int sinks);
+
+/* sv_paged_attention with first tokens that stay visible beside the window: a
+ * row at place p sees the tokens j <= p with j > p - window or j < sinks (all
+ * j <= p with window 0).  Tokens between the two are not read, and the work is
+ * divided by what a row sees rather than by max_kv_len.
+ *   sinks      >= 0. */
+int sv_paged_attention_sinks(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
+                             int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
+                             const int32_t* kv_len, int max_q_len, int max_kv_len, float scale, int window, int sinks,
+                             void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
+                             size_t workspace_bytes);
+
+/* Bytes of workspace that sv_paged_attention_shared needs (256: none); 0 for
+ * sizes that the call would reject. */
+size_t sv_paged_attention_shared_workspace_size(int B, int T, int groups, int q_heads, int kv_heads, int head_dim,
+                                                int max_q_len, int max_group_len, int max_shared_len, int max_own_len);
+
+/* sv_paged_attention (without a window) for requests whose first tokens are the
+ * same: group g is the requests group_start[g] .. group_start[g+1] - 1, whose
+ * first shared_len[g] tokens are read once for all of them, through the page
+ * table row of the first of them.  The rows of the others should hold the same
+ * pages there, or copies (of a page that is shared in part, say): the result is
+ * then that of sv_paged_attention but for roundings.  A row sees a shared token
+ * j if j <= its place, as any other.
+ *   groups     0: nothing is shared.
+ *   group_start    int32 [groups + 1], ascending, within 0..B; requests outside
+ *              group_start[0] .. group_start[groups] - 1 share nothing.
+ *   shared_len     int32 [groups]; negative counts as 0.  The first request's row
+ *              has to hold the shared pages also where that request has no rows,
+ *              or a kv_len below shared_len.
+ *   max_q_len, max_group_len, max_shared_len, max_own_len   the most new tokens
+ *              of a request and of a group, the largest shared_len, and the
+ *              largest number of tokens of a request that are not shared, as far
+ *              as the caller knows them (0: not known; then contexts are not
+ *              divided).  They choose how the work is divided, as in
+ *              sv_paged_attention. */
+int sv_paged_attention_shared(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
+                              const int32_t* kv_len, int groups, const int32_t* group_start, const int32_t* shared_len,
+                              int max_q_len, int max_group_len, int max_shared_len, int max_own_len, float scale,
+                              void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse, void* workspace,
+                              size_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,10 +5,15 @@ Plain float64 numpy and python lists, one step at a time, from the definitions:
 
 * a head's row x becomes R(x r w), r = (mean x^2 + eps)^-1/2, R the rotation of
   ``oracle.attn.rope``; its gradients by the chain rule, matrix by matrix;
+* a row at place p sees the tokens j <= p of its request, with a window those with
+  j > p - window or j < sinks; the first tokens of a group's requests are those
+  of its first request's row of the page table;
 * pages of a cache move between requests' rows of a page table and a stack, one
   page at a time.
 """
 from __future__ import annotations
+
+import math
 
 import numpy as np
 
@@ -78,3 +83,35 @@ def slots(table, held, kv_len, query_start, page_size, capacity):
             page = table[b][p // page_size] if 0 <= p // page_size < held[b] else -1
             where.append(page * page_size + p % page_size if 0 <= page < capacity else -1)
     return where, place
+
+
+def attention(q, cache, query_start, kv_len, scale, window=0, sinks=0, group_start=(0,), shared_len=()):
+    """As ``oracle.attn.attention``, with sinks and with groups of requests that share their first tokens."""
+    q = np.asarray(q, np.float64)
+    T, Hq, D = q.shape
+    g = Hq // cache["k"].shape[2]
+    out, spread = np.full((T, Hq, D), np.nan), np.full((T, Hq, D), np.nan)
+    lse, size = np.full((T, Hq), np.nan), np.zeros((T, Hq))
+    for b in range(len(kv_len)):
+        first, shared = b, 0
+        for i, n in enumerate(shared_len):
+            if group_start[i] <= b < group_start[i + 1]:
+                first, shared = group_start[i], n
+        for r in range(query_start[b], query_start[b + 1]):
+            p = oa.place_of(query_start, np.maximum(kv_len, 0), b, r - query_start[b])
+            seen = [j for j in range(p + 1) if window == 0 or j > p - window or j < sinks]
+            at = [oa.slot_of(cache, first if j < shared else b, j) for j in seen]
+            at = [x for x in at if x is not None]
+            if not at:
+                out[r], spread[r], lse[r] = 0, 0, -np.inf
+                continue
+            k, v = (cache[n][[x[0] for x in at], [x[1] for x in at]] for n in "kv")
+            for h in range(Hq):
+                s = scale * (k[:, h // g] @ q[r, h])
+                top = s.max()
+                w = np.exp(s - top)
+                lse[r, h] = top + math.log(w.sum())
+                out[r, h] = (w @ v[:, h // g]) / w.sum()
+                spread[r, h] = (w @ np.abs(v[:, h // g])) / w.sum()
+                size[r, h] = scale * (np.abs(k[:, h // g]) @ np.abs(q[r, h])).max()
+    return dict(out=out, lse=lse, spread=spread, size=size)

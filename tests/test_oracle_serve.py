@@ -73,3 +73,43 @@ def test_shared_pages_stay_and_refusals_go_in_order():
     assert os_.pages(table, held, free, [0, 8, 8], 2, 10, shared=[2, 2, 2]) == [1, 1, 0]
     assert table == [[7, 8, -1, -1], [7, 8, 9, 0], [7, 8, -1, -1]] and held == [2, 4, 2] and free == [1]
     assert os_.slots(table, held, [0, 8, 5], [0, 0, 2, 4], 2, 9) == ([0, 1, 17, -1], [6, 7, 3, 4])
+
+
+def small_cache(seed, B=3, pages=9, size=4, heads=2, D=8):
+    rng = np.random.default_rng(seed)
+    c = dict(k=rng.normal(size=(pages, size, heads, D)), v=rng.normal(size=(pages, size, heads, D)),
+             table=rng.permutation(pages)[:9].reshape(3, 3))
+    return c, rng.normal(size=(6, 4, D))
+
+
+def test_attention_without_sinks_and_groups_is_the_older_oracle():
+    c, q = small_cache(0)
+    for window in (0, 1, 3):
+        a = oa.attention(q, c, [0, 1, 3, 6], [12, 2, 9], 0.4, window)
+        b = os_.attention(q, c, [0, 1, 3, 6], [12, 2, 9], 0.4, window)
+        assert all(np.allclose(a[n], b[n], atol=1e-14) for n in a)
+
+
+def test_attention_sinks_join_what_is_before_the_window():
+    """Weights of two disjoint sets of tokens add: the window's result and that of the first tokens, by their lse."""
+    c, q = small_cache(1)
+    start, length = [0, 1, 1, 1], [12, 0, 0]
+    whole = os_.attention(q[:1], c, start, length, 0.4, 5, 3)
+    near = os_.attention(q[:1], c, start, length, 0.4, 5)
+    first = os_.attention(q[:1], c, start, [3, 0, 0], 0.4)
+    a, b = np.exp(near["lse"] - whole["lse"]), np.exp(first["lse"] - whole["lse"])
+    assert np.allclose(a + b, 1) and np.allclose(a[..., None] * near["out"] + b[..., None] * first["out"], whole["out"])
+    assert np.allclose(os_.attention(q[:1], c, start, length, 0.4, 9, 3)["out"], os_.attention(q[:1], c, start, length, 0.4)["out"])
+
+
+def test_attention_reads_shared_tokens_from_the_first_row():
+    c, q = small_cache(2)
+    start, length = [0, 2, 4, 6], [5, 9, 10]
+    shared = os_.attention(q, c, start, length, 0.4, group_start=[0, 1, 3], shared_len=[2, 6])
+    wide = dict(c, table=c["table"].copy())
+    wide["table"][2, 0] = c["table"][1, 0]  # the third request's tokens 0 .. 3, and of the next page 4 and 5
+    k = {n: c[n].copy() for n in "kv"}
+    for n in "kv":
+        k[n][c["table"][2, 1], :2] = c[n][c["table"][1, 1], :2]
+    want = oa.attention(q, dict(wide, **k), start, length, 0.4)
+    assert all(np.allclose(shared[n], want[n], atol=1e-14) for n in want)

@@ -117,3 +117,75 @@ def test_binding_refuses_host_tensors():
                  lambda: sv.sv_kv_pages(i(1, 2), i(1), i(3), i(1), i(1), page_size=16)):
         with pytest.raises(ValueError, match="HIP device"):
             call()
+
+
+def sinks(c=None, **kw):
+    a = dict(stream=None, B=4, T=9, q_heads=4, q=FAKE, qt=256, qh=64)
+    b = dict(qs=FAKE, kl=FAKE, max_q=5, max_kv=100, scale=0.125, window=0, sinks=4, out=FAKE, ot=256, oh=64, lse=None,
+             ws=FAKE, bytes=1 << 40)
+    c = cache() if c is None else c
+    a.update({k: v for k, v in kw.items() if k in a})
+    b.update({k: v for k, v in kw.items() if k in b})
+    return attn._attn_lib().sv_paged_attention_sinks(*a.values(), ctypes.addressof(c), *b.values())
+
+
+def shared(c=None, **kw):
+    a = dict(stream=None, B=4, T=9, q_heads=4, q=FAKE, qt=256, qh=64)
+    b = dict(qs=FAKE, kl=FAKE, groups=2, gs=FAKE, sl=FAKE, max_q=5, max_group=5, max_shared=100, max_own=100, scale=0.125,
+             out=FAKE, ot=256, oh=64, lse=None, ws=FAKE, bytes=1 << 40)
+    c = cache() if c is None else c
+    a.update({k: v for k, v in kw.items() if k in a})
+    b.update({k: v for k, v in kw.items() if k in b})
+    return attn._attn_lib().sv_paged_attention_shared(*a.values(), ctypes.addressof(c), *b.values())
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHES)
+def test_bad_caches_are_refused_by_the_attention_calls(kw, status):
+    for call in (sinks, shared):
+        assert call(cache(**kw)) == status, call.__name__
+
+
+ATTENTION = [
+    (dict(B=-1), -1), (dict(T=-1), -1), (dict(B=(1 << 18) + 1), -2), (dict(q_heads=3), -1), (dict(q_heads=0), -1),
+    (dict(q_heads=1026), -2), (dict(q=None), -1), (dict(q=FAKE + 8), -1), (dict(out=None), -1), (dict(out=FAKE + 2), -1),
+    (dict(qt=250), -1), (dict(qh=4), -1), (dict(ot=-8), -1), (dict(ot=0), -1), (dict(oh=32), -1), (dict(qs=None), -1),
+    (dict(kl=None), -1), (dict(max_q=-1), -1), (dict(scale=0.0), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1),
+    (dict(T=0, q=None), 0), (dict(B=0, q=None), 0),
+]
+
+
+@pytest.mark.parametrize("kw,status", ATTENTION + [
+    (dict(max_kv=-1), -1), (dict(window=-1), -1), (dict(sinks=-1), -1), (dict(sinks=-1, T=0), -1),
+    (dict(ws=None, max_kv=5000), -3), (dict(ws=FAKE + 4, max_kv=5000), -3),
+    (dict(bytes=8, max_kv=50000, window=3000), -3),
+])
+def test_sinks_refuse_before_launch(kw, status):
+    assert sinks(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", ATTENTION + [
+    (dict(max_group=-1), -1), (dict(max_shared=-1), -1), (dict(max_own=-1), -1), (dict(groups=-1), -1),
+    (dict(groups=(1 << 18) + 1), -2), (dict(gs=None), -1), (dict(sl=None), -1), (dict(ws=None), -3), (dict(ws=FAKE + 4), -3),
+    (dict(bytes=8), -3), (dict(groups=0, gs=None, sl=None, ws=None, max_own=5000), -3),
+])
+def test_shared_refuses_before_launch(kw, status):
+    assert shared(**kw) == status
+
+
+def test_attention_workspace_sizes():
+    size = sv.sv_paged_attention_sinks_workspace_size
+    plain = sv.sv_paged_attention_workspace_size
+    assert size(4, 4, 32, 8, 128, 1, 100000, 0, 4) == plain(4, 4, 32, 8, 128, 1, 100000)
+    assert size(4, 4, 32, 8, 128, 1, 100000, 200, 4) == 256  # what a row sees is not divided
+    assert 256 < size(4, 4, 32, 8, 128, 1, 100000, 4096, 4) < plain(4, 4, 32, 8, 128, 1, 100000)
+    assert size(4, 4, 32, 8, 128, 1, 2 ** 40, 2 ** 40, 2 ** 40) == plain(4, 4, 32, 8, 128, 1, 2 ** 40)
+    for bad in ((-1, 4, 32, 8, 128, 1, 5, 1, 1), (4, 4, 30, 8, 128, 1, 5, 1, 1), (4, 4, 32, 8, 128, 1, 5, -1, 1),
+                (4, 4, 32, 8, 128, 1, 5, 1, -1)):
+        assert size(*bad) == 0
+    size = sv.sv_paged_attention_shared_workspace_size
+    assert size(4, 4, 1, 32, 8, 128, 1, 4, 100, 100) >= 256 + 2 * 4 * 32 * (128 * 4 + 8)
+    assert size(4, 4, 0, 32, 8, 128, 1, 4, 100, 5000) == plain(4, 4, 32, 8, 128, 1, 5000)
+    for bad in ((-1, 4, 1, 32, 8, 128), (4, 4, -1, 32, 8, 128), (4, 4, (1 << 18) + 1, 32, 8, 128), (4, 4, 1, 30, 8, 128),
+                (4, 4, 1, 32, 8, 128, -1), (4, 4, 1, 32, 8, 128, 1, -1), (4, 4, 1, 32, 8, 128, 1, 1, -1),
+                (4, 4, 1, 32, 8, 128, 1, 1, 1, -1)):
+        assert size(*bad) == 0, bad
