@@ -91,7 +91,9 @@ int check_attention_sizes(int B, int T, int q_heads, int kv_heads, int head_dim,
 }
 
 // A norm's arguments; rows are checked by row_strides_ok.
-bool norm_ok(int weight_dtype, float eps) { return rows_dtype_ok(weight_dtype) && eps > 0.f && isfinite(eps); }
+bool norm_ok(int weight_dtype, float eps) {
+  return rows_dtype_ok(weight_dtype) && eps >= 1.17549435e-38f && isfinite(eps);
+}
 
 int append(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, int layout, const double* freq,
            float mscale, const int64_t* positions, const NormWeights* norm, const RowsIn& q, const RowsOut& q_out,
@@ -131,7 +133,7 @@ int append(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, i
   a.kv_len = kv_len;
   a.cache = view_of(cache);
   a.normed = norm != nullptr;
-  a.norm = norm ? *norm : NormWeights{nullptr, nullptr, SV_F32, 1.f};
+  a.norm = norm ? *norm : NormWeights{nullptr, nullptr, SV_F32, 1.f, 1.};
   return to_status(launch_append(a, dtype, cache->dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -303,7 +305,8 @@ int sv_kv_append_normed(void* stream, int B, int T, int q_heads, int dtype, int 
                         const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
                         int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,
                         const int32_t* kv_len, const sv_paged_cache* cache) {
-  const NormWeights norm = {q_weight, k_weight, weight_dtype, eps};
+  NormWeights norm = {q_weight, k_weight, weight_dtype, eps, 0.};
+  if (cache && cache->head_dim > 0) norm.inv_dim = 1. / cache->head_dim;
   return append(stream, B, T, q_heads, dtype, rotary_dim, layout, freq, mscale, positions, &norm,
                 {q, q_token_stride, q_head_stride}, {q_out, q_out_token_stride, q_out_head_stride},
                 {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, query_start, kv_len, cache);
@@ -315,7 +318,7 @@ int sv_qk_norm_rope(void* stream, int T, int q_heads, int k_heads, int head_dim,
                     const void* k_weight, float eps, const int64_t* positions, const double* freq, float mscale,
                     void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
                     int64_t k_out_token_stride, int64_t k_out_head_stride) {
-  NormRopeArgs a = {T, q_heads, k_heads, head_dim, rotary_dim, layout, {q_weight, k_weight, weight_dtype, eps}};
+  NormRopeArgs a = {T, q_heads, k_heads, head_dim, rotary_dim, layout, {q_weight, k_weight, weight_dtype, eps, 1. / head_dim}};
   a.q = {q, q_token_stride, q_head_stride};
   a.k = {k, k_token_stride, k_head_stride};
   a.q_out = {q_out, q_out_token_stride, q_out_head_stride};
@@ -342,7 +345,7 @@ int sv_qk_norm_rope_backward(void* stream, int T, int q_heads, int k_heads, int 
                              const double* freq, float mscale, void* dq, int64_t dq_token_stride,
                              int64_t dq_head_stride, void* dk, int64_t dk_token_stride, int64_t dk_head_stride,
                              float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes) {
-  NormRopeArgs a = {T, q_heads, k_heads, head_dim, rotary_dim, layout, {q_weight, k_weight, weight_dtype, eps}};
+  NormRopeArgs a = {T, q_heads, k_heads, head_dim, rotary_dim, layout, {q_weight, k_weight, weight_dtype, eps, 1. / head_dim}};
   a.q = {q, q_token_stride, q_head_stride};
   a.k = {k, k_token_stride, k_head_stride};
   a.dq = {dq_out, dq_out_token_stride, dq_out_head_stride};

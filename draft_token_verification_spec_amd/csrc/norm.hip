@@ -19,58 +19,83 @@ namespace sv {
 
 namespace {
 
-template <bool VEC, typename ET>
+// A thread's items, heads of a workgroup's rows in turn: the i-th of the
+// workgroup's groups starts at the i-th.
+struct Item {
+  int row, head;
+  __device__ __forceinline__ void settle(int total) {
+    while (head >= total) head -= total, ++row;
+  }
+};
+
+// mscale * (cos, sin) of the angles of rows t0 .. t0 + rows - 1.
+template <int ROWS>
+__device__ __forceinline__ void angles_of_rows(float2 (*cs)[kMaxPairs], const NormRopeArgs& a, int t0, int rows, float sign) {
+  const int pairs = a.rotary >> 1;
+  for (int i = threadIdx.x; i < ROWS * pairs; i += kRopeThreads) {
+    const int r = ROWS == 1 ? 0 : i / pairs, e = i - r * pairs;
+    if (r < rows) cs[r][e] = turn_of(double(a.positions[t0 + r]), a.freq[e], a.mscale, sign);
+  }
+}
+
+template <int ROWS, bool VEC, typename ET>
 __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(NormRopeArgs a) {
-  __shared__ float2 cs[kMaxPairs];
+  __shared__ float2 cs[ROWS][kMaxPairs];
   __shared__ float w[2][SV_ATTN_MAX_HEAD_DIM];
-  const int t = blockIdx.x;
+  const int t0 = blockIdx.x * ROWS, rows = min(ROWS, a.T - t0);
   stage_weights(w, a.norm, a.D);
-  make_angles(cs, a.freq, a.rotary >> 1, a.rotary ? double(a.positions[t]) : 0., a.mscale, 1.f);
+  angles_of_rows<ROWS>(cs, a, t0, rows, 1.f);
   __syncthreads();
   const int lg = head_lanes_log2(a.D), lanes = 1 << lg;
   const int e0 = (threadIdx.x & (lanes - 1)) * 8;
   const int total = a.q_heads + a.k_heads;
-  for (int g = threadIdx.x >> lg; g < total; g += kRopeThreads >> lg) {
-    const bool key = g >= a.q_heads;
-    const int h = key ? g - a.q_heads : g;
+  Item it = {0, int(threadIdx.x >> lg)};
+  for (it.settle(total); it.row < rows; it.head += kRopeThreads >> lg, it.settle(total)) {
+    const bool key = it.head >= a.q_heads;
+    const int h = key ? it.head - a.q_heads : it.head;
     const RowsIn& in = key ? a.k : a.q;
     const RowsOut& out = key ? a.k_out : a.q_out;
+    const int64_t t = t0 + it.row;
     float y[8] = {};
-    normed8<VEC>(static_cast<const ET*>(in.p) + int64_t(t) * in.token + h * in.head, e0, a.D, a.rotary, a.layout, cs,
-                 w[key], a.norm.eps, lanes, y);
-    if (e0 < a.D) put8<VEC>(static_cast<ET*>(out.p) + int64_t(t) * out.token + h * out.head, e0, a.D, y);
+    normed8<VEC>(static_cast<const ET*>(in.p) + t * in.token + h * in.head, e0, a.D, a.rotary, a.layout, cs[it.row],
+                 w[key], a.norm, lanes, y);
+    if (e0 < a.D) put8<VEC>(static_cast<ET*>(out.p) + t * out.token + h * out.head, e0, a.D, y);
   }
 }
 
 constexpr int kMostParts = 1024;  // workgroups of the backward pass: 16 waves a compute unit
 
-template <bool VEC, typename ET>
+template <int ROWS, bool VEC, typename ET>
 __global__ __launch_bounds__(kRopeThreads) void norm_rope_backward_kernel(NormRopeArgs a) {
-  __shared__ float2 cs[2][kMaxPairs];
+  __shared__ float2 cs[2][ROWS][kMaxPairs];
   __shared__ float w[2][SV_ATTN_MAX_HEAD_DIM];
   __shared__ float sums[kRopeThreads / 64][2][SV_ATTN_MAX_HEAD_DIM];
   const int lg = head_lanes_log2(a.D), lanes = 1 << lg;
   const int e0 = (threadIdx.x & (lanes - 1)) * 8;
   const int total = a.q_heads + a.k_heads;
+  const float inv_dim = float(a.norm.inv_dim);
   float dw[2][8] = {};
   stage_weights(w, a.norm, a.D);
   int buf = 0;
-  // (the barrier of a row ends every read of the angles of the row before)
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
-    make_angles(cs[buf], a.freq, a.rotary >> 1, a.rotary ? double(a.positions[t]) : 0., a.mscale, -1.f);
+  // (the barrier of some rows ends every read of the angles of those before)
+  for (int t0 = blockIdx.x * ROWS; t0 < a.T; t0 += gridDim.x * ROWS, buf ^= 1) {
+    const int rows = min(ROWS, a.T - t0);
+    angles_of_rows<ROWS>(cs[buf], a, t0, rows, -1.f);
     __syncthreads();
-    for (int i = threadIdx.x >> lg; i < total; i += kRopeThreads >> lg) {
-      const bool key = i >= a.q_heads;
-      const int h = key ? i - a.q_heads : i;
+    Item it = {0, int(threadIdx.x >> lg)};
+    for (it.settle(total); it.row < rows; it.head += kRopeThreads >> lg, it.settle(total)) {
+      const bool key = it.head >= a.q_heads;
+      const int h = key ? it.head - a.q_heads : it.head;
       const RowsIn& in = key ? a.k : a.q;
       const RowsIn& grad = key ? a.dk : a.dq;
       const RowsOut& out = key ? a.k_out : a.q_out;
-      const ET* px = static_cast<const ET*>(in.p) + int64_t(t) * in.token + h * in.head;
-      const ET* pg = static_cast<const ET*>(grad.p) + int64_t(t) * grad.token + h * grad.head;
+      const int64_t t = t0 + it.row;
+      const ET* px = static_cast<const ET*>(in.p) + t * in.token + h * in.head;
+      const ET* pg = static_cast<const ET*>(grad.p) + t * grad.token + h * grad.head;
       float u[8] = {}, g[8] = {};
       load_pairs8<VEC>(px, e0, a.D, 0, a.layout, u, g);
-      if (e0 < a.D) turned8<VEC>(pg, e0, a.D, a.rotary, a.layout, cs[buf], g);
-      const float r = inverse_norm(u, a.D, a.norm.eps, lanes);
+      if (e0 < a.D) turned8<VEC>(pg, e0, a.D, a.rotary, a.layout, cs[buf][it.row], g);
+      const float r = inverse_norm(u, a.norm, lanes);
       float dot = 0.f, y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -82,10 +107,10 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_backward_kernel(NormRo
         y[j] = VEC || e0 + j < a.D ? g[j] * w[key][min(e0 + j, SV_ATTN_MAX_HEAD_DIM - 1)] : 0.f;
         dot = fmaf(y[j], u[j], dot);
       }
-      const float c = group_sum(dot, lanes) / float(a.D);
+      const float c = group_sum(dot, lanes) * inv_dim;
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = r * (y[j] - u[j] * c);
-      if (e0 < a.D) put8<VEC>(static_cast<ET*>(out.p) + int64_t(t) * out.token + h * out.head, e0, a.D, y);
+      if (e0 < a.D) put8<VEC>(static_cast<ET*>(out.p) + t * out.token + h * out.head, e0, a.D, y);
     }
   }
   if (!a.part) return;
@@ -137,44 +162,49 @@ bool vec_of(const NormRopeArgs& a, int elem, bool backward) {
   return vec;
 }
 
+// Rows that a workgroup takes at a time: several where there are enough to fill
+// the card with.
+constexpr int kManyRowsAtATime = 4;
+bool many(int T) { return T >= 1024 * kManyRowsAtATime; }
+
+template <int ROWS, bool VEC, typename ET>
+void launch_rows_of(const NormRopeArgs& a, bool backward, hipStream_t stream) {
+  const int blocks = (a.T + ROWS - 1) / ROWS;
+  if (backward)
+    hipLaunchKernelGGL((norm_rope_backward_kernel<ROWS, VEC, ET>), dim3(norm_parts(a.T)), dim3(kRopeThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((norm_rope_kernel<ROWS, VEC, ET>), dim3(blocks), dim3(kRopeThreads), 0, stream, a);
+}
+
+template <bool VEC, typename ET>
+void launch_type(const NormRopeArgs& a, bool backward, hipStream_t stream) {
+  many(a.T) ? launch_rows_of<kManyRowsAtATime, VEC, ET>(a, backward, stream) : launch_rows_of<1, VEC, ET>(a, backward, stream);
+}
+
+void launch_of(const NormRopeArgs& a, int dtype, bool backward, hipStream_t stream) {
+  const bool vec = vec_of(a, dtype == SV_BF16 ? 2 : 4, backward);
+  if (dtype == SV_BF16)
+    vec ? launch_type<true, uint16_t>(a, backward, stream) : launch_type<false, uint16_t>(a, backward, stream);
+  else
+    vec ? launch_type<true, float>(a, backward, stream) : launch_type<false, float>(a, backward, stream);
+}
+
 }  // namespace
 
-int norm_parts(int T) { return T < kMostParts ? T : kMostParts; }
+int norm_parts(int T) {
+  const int blocks = many(T) ? (T + kManyRowsAtATime - 1) / kManyRowsAtATime : T;
+  return blocks < kMostParts ? blocks : kMostParts;
+}
 
 hipError_t launch_norm(const NormRopeArgs& a, int dtype, hipStream_t stream) {
-  const dim3 grid(a.T), block(kRopeThreads);
-  if (dtype == SV_BF16) {
-    if (vec_of(a, 2, false))
-      hipLaunchKernelGGL((norm_rope_kernel<true, uint16_t>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((norm_rope_kernel<false, uint16_t>), grid, block, 0, stream, a);
-  } else {
-    if (vec_of(a, 4, false))
-      hipLaunchKernelGGL((norm_rope_kernel<true, float>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((norm_rope_kernel<false, float>), grid, block, 0, stream, a);
-  }
+  launch_of(a, dtype, false, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_norm_backward(const NormRopeArgs& a, int dtype, hipStream_t stream) {
-  const int parts = norm_parts(a.T);
-  const dim3 grid(parts), block(kRopeThreads);
-  if (parts > 0) {
-    if (dtype == SV_BF16) {
-      if (vec_of(a, 2, true))
-        hipLaunchKernelGGL((norm_rope_backward_kernel<true, uint16_t>), grid, block, 0, stream, a);
-      else
-        hipLaunchKernelGGL((norm_rope_backward_kernel<false, uint16_t>), grid, block, 0, stream, a);
-    } else {
-      if (vec_of(a, 4, true))
-        hipLaunchKernelGGL((norm_rope_backward_kernel<true, float>), grid, block, 0, stream, a);
-      else
-        hipLaunchKernelGGL((norm_rope_backward_kernel<false, float>), grid, block, 0, stream, a);
-    }
-  }
+  if (a.T > 0) launch_of(a, dtype, true, stream);
   if (a.dq_weight || a.dk_weight)
-    hipLaunchKernelGGL(weight_gradient_kernel, dim3((2 * a.D + 15) / 16), dim3(kJoinThreads), 0, stream, a, parts);
+    hipLaunchKernelGGL(weight_gradient_kernel, dim3((2 * a.D + 15) / 16), dim3(kJoinThreads), 0, stream, a, norm_parts(a.T));
   return hipGetLastError();
 }
 

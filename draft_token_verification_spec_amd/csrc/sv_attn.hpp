@@ -33,6 +33,7 @@ struct NormWeights {
   const void* k;
   int dtype;
   float eps;
+  double inv_dim;  // 1 / head_dim
 };
 
 // Queries and keys [T, heads, D] normed and turned, or (launch_norm_backward)
@@ -47,9 +48,9 @@ struct NormRopeArgs {
   const int64_t* positions;
   const double* freq;
   float mscale;
-  float* part;        // [norm_parts(T)][2][D], the weights' gradients of a workgroup's rows
-  float* dq_weight;   // nullable
-  float* dk_weight;   // nullable
+  float* part;       // [norm_parts(T)][2][D], the weights' gradients of a workgroup's rows
+  float* dq_weight;  // nullable
+  float* dk_weight;  // nullable
 };
 int norm_parts(int T);  // workgroups of the backward pass
 hipError_t launch_norm(const NormRopeArgs& a, int dtype, hipStream_t stream);

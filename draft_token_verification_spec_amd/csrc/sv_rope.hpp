@@ -9,22 +9,30 @@ namespace sv {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxPairs = SV_ATTN_MAX_HEAD_DIM / 2;
 
-// mscale * (cos, sin) of the row's angles, by the whole workgroup.
+// Half turns of the angle position * f without its whole turns, in -1..1.
+__device__ __forceinline__ double half_turns(double position, double f) {
+  constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLow = -9.839338337591243e-18;  // 1 / (2 pi) to 106 bits
+  const double angle = position * f, low = fma(position, f, -angle);
+  double turns = fma(angle, kInv2Pi, -rint(angle * kInv2Pi));
+  turns += fma(angle, kInv2PiLow, low * kInv2Pi);
+  return 2 * turns;
+}
+
+// mscale * (cos, sin) of the angle position * f.
+__device__ __forceinline__ float2 turn_of(double position, double f, float mscale, float sign) {
+  constexpr double kPi = 3.141592653589793;
+  // what binary32 drops of the half turns is put back to first order
+  const double halves = half_turns(position, f);
+  const float near = float(halves), rest = float((halves - near) * kPi);
+  float s, c;
+  sincospif(near, &s, &c);
+  return make_float2(fmaf(-rest, s, c) * mscale, fmaf(rest, c, s) * mscale * sign);
+}
+
+// The same of the row's angles, by the whole workgroup.
 __device__ __forceinline__ void make_angles(float2* cs, const double* freq, int pairs, double position, float mscale,
                                             float sign) {
-  constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLow = -9.839338337591243e-18;  // 1 / (2 pi) to 106 bits
-  constexpr double kPi = 3.141592653589793;
-  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) {
-    const double f = freq[i], angle = position * f, low = fma(position, f, -angle);
-    double turns = fma(angle, kInv2Pi, -rint(angle * kInv2Pi));
-    turns += fma(angle, kInv2PiLow, low * kInv2Pi);
-    // what binary32 drops of the half turns is put back to first order
-    const double halves = 2 * turns;
-    const float near = float(halves), rest = float((halves - near) * kPi);
-    float s, c;
-    sincospif(near, &s, &c);
-    cs[i] = make_float2(fmaf(-rest, s, c) * mscale, fmaf(rest, c, s) * mscale * sign);
-  }
+  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) cs[i] = turn_of(position, freq[i], mscale, sign);
 }
 
 // Channels e0 .. e0 + 7 of one head's row x, turned.  VEC: x is 16-byte
@@ -104,12 +112,15 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
 }
 
 // (mean of squares + eps)^-1/2 of a row whose 8 channels a lane are y (zeros
-// beyond the row).
-__device__ __forceinline__ float inverse_norm(const float (&y)[8], int D, float eps, int lanes) {
-  float sq = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sq = fmaf(y[j], y[j], sq);
-  return 1.f / sqrtf(group_sum(sq, lanes) / float(D) + eps);
+// beyond the row).  The squares are summed pairwise in binary32; what follows is
+// one step of Newton's method in binary64, five operations, so that the result
+// adds no more than its own rounding to the sum's.
+__device__ __forceinline__ float inverse_norm(const float (&y)[8], const NormWeights& n, int lanes) {
+  const auto two = [&](int j) { return fmaf(y[j], y[j], y[j + 1] * y[j + 1]); };
+  const float sq = (two(0) + two(2)) + (two(4) + two(6));
+  const double m = double(group_sum(sq, lanes)) * n.inv_dim + n.eps;
+  const double r = __builtin_amdgcn_rsqf(float(m));
+  return float(r * (1.5 - 0.5 * m * r * r));
 }
 
 // The row's channels e0 .. e0 + 7 (zeros beyond it) and those that they are
@@ -134,32 +145,36 @@ __device__ __forceinline__ void load_pairs8(const ET* x, int e0, int D, int rota
   }
 }
 
-// y, with what it is paired with in z, times r and the weights, and turned.
+// y, with what it is paired with in z, times the weights, turned, and times r:
+// in this order the first product is exact for bf16 rows and weights, and the
+// row's sum is needed last.  (Explicitly fused, so that a row's bits do not depend
+// on its alignment.)
 template <bool VEC>
 __device__ __forceinline__ void normed_and_turned8(float (&y)[8], float (&z)[8], int e0, int D, int rotary, int layout,
                                                    const float2* cs, const float* w, float r) {
   const int half = rotary >> 1;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (VEC || e0 + j < D) y[j] *= r * w[e0 + j];
+    if (VEC || e0 + j < D) y[j] *= w[e0 + j];
   if (VEC) {
-    if (e0 >= rotary) return;
-    if (layout == SV_ROPE_HALF) {
-      const bool first = e0 < half;
-      const int i0 = first ? e0 : e0 - half, o0 = first ? e0 + half : i0;
+    if (e0 < rotary) {
+      if (layout == SV_ROPE_HALF) {
+        const bool first = e0 < half;
+        const int i0 = first ? e0 : e0 - half, o0 = first ? e0 + half : i0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 t = cs[i0 + j];
-        z[j] *= r * w[o0 + j];
-        y[j] = first ? y[j] * t.x - z[j] * t.y : z[j] * t.y + y[j] * t.x;
-      }
-    } else {
+        for (int j = 0; j < 8; ++j) {
+          const float2 t = cs[i0 + j];
+          z[j] *= w[o0 + j];
+          y[j] = fmaf(y[j], t.x, first ? -(z[j] * t.y) : z[j] * t.y);
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float2 t = cs[(e0 + j) >> 1];
-        const float a = y[j], c = y[j + 1];
-        y[j] = a * t.x - c * t.y;
-        y[j + 1] = a * t.y + c * t.x;
+        for (int j = 0; j < 8; j += 2) {
+          const float2 t = cs[(e0 + j) >> 1];
+          const float a = y[j], c = y[j + 1];
+          y[j] = fmaf(a, t.x, -(c * t.y));
+          y[j + 1] = fmaf(c, t.x, a * t.y);
+        }
       }
     }
   } else {
@@ -170,20 +185,69 @@ __device__ __forceinline__ void normed_and_turned8(float (&y)[8], float (&z)[8],
       const bool first = layout == SV_ROPE_HALF ? e < half : (e & 1) == 0;
       const int other = layout == SV_ROPE_HALF ? (first ? e + half : e - half) : e ^ 1;
       const float2 t = cs[layout == SV_ROPE_HALF ? (first ? e : other) : e >> 1];
-      z[j] *= r * w[other];
-      y[j] = first ? y[j] * t.x - z[j] * t.y : z[j] * t.y + y[j] * t.x;
+      z[j] *= w[other];
+      y[j] = fmaf(y[j], t.x, first ? -(z[j] * t.y) : z[j] * t.y);
     }
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] *= r;
 }
 
 // One head's row x normed and turned, by all lanes of its group.
 template <bool VEC, typename ET>
 __device__ __forceinline__ void normed8(const ET* x, int e0, int D, int rotary, int layout, const float2* cs,
-                                        const float* w, float eps, int lanes, float (&y)[8]) {
+                                        const float* w, const NormWeights& n, int lanes, float (&y)[8]) {
   float z[8] = {};
   load_pairs8<VEC>(x, e0, D, rotary, layout, y, z);
-  const float r = inverse_norm(y, D, eps, lanes);
+  const float r = inverse_norm(y, n, lanes);
   if (e0 < D) normed_and_turned8<VEC>(y, z, e0, D, rotary, layout, cs, w, r);
+}
+
+// A number that rounds to e4m3 as x does: x without what binary32 has no place
+// for, its last bit set where something is missing.  (Beyond binary32's normal
+// numbers: the nearest one.)
+__device__ __forceinline__ float shortened(double x) {
+  const uint64_t bits = __double_as_longlong(x);
+  const uint32_t high = uint32_t(bits >> 32), low = uint32_t(bits);
+  const uint32_t size = high & 0x7fffffffu;
+  if (size - (897u << 20) >= 253u << 20) return float(x);
+  return __uint_as_float((high & 0x80000000u) | ((size - (896u << 20)) << 3) | (low >> 29) | ((low & 0x1fffffffu) != 0));
+}
+
+// One head's row x normed and turned in binary64, by all lanes of its group:
+// keys, which are stored once and read by every later row, are so the nearest
+// 8-bit values (FP8; in binary32 some 10^-6 of them are not), or the nearest
+// binary32 ones on their way to bf16.  cs: binary64 too.
+template <bool VEC, bool FP8, typename ET>
+__device__ __forceinline__ void normed_key8(const ET* x, int e0, int D, int rotary, int layout, const double2* cs,
+                                            const float* w, const NormWeights& n, int lanes, float (&y)[8]) {
+  float z[8] = {};
+  load_pairs8<VEC>(x, e0, D, rotary, layout, y, z);
+  if (VEC && layout == SV_ROPE_INTERLEAVED) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = y[j ^ 1];
+  }
+  double sq = 0.;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sq = fma(double(y[j]), double(y[j]), sq);
+  for (int o = lanes >> 1; o >= 1; o >>= 1) sq += __shfl_xor(sq, o, 64);
+  const double m = sq * n.inv_dim + n.eps, near = __builtin_amdgcn_rsqf(float(m));
+  const double r = near * (1.5 - 0.5 * m * near * near);
+  const int half = rotary >> 1;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int e = e0 + j;
+    if (e >= D) continue;
+    double v = double(y[j]) * w[e];
+    if (e < rotary) {
+      const bool first = layout == SV_ROPE_HALF ? e < half : (e & 1) == 0;
+      const int other = layout == SV_ROPE_HALF ? (first ? e + half : e - half) : e ^ 1;
+      const double2 t = cs[layout == SV_ROPE_HALF ? (first ? e : other) : e >> 1];
+      const double u = double(z[j]) * w[other] * t.y;
+      v = fma(v, t.x, first ? -u : u);
+    }
+    y[j] = FP8 ? shortened(v * r) : float(v * r);
+  }
 }
 
 // Least e >= -117 with amax <= 448 * 2^e: 448 = 0.875 * 2^9 (-9 for 0).  The

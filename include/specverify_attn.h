@@ -165,7 +165,7 @@ int sv_kv_append(void* stream, int B, int T, int q_heads, int dtype, int rotary_
  *              Heads 0: there are no queries, or no keys.
  *   q_weight, k_weight   [head_dim], SV_F32 or SV_BF16 (weight_dtype); NULL:
  *              all 1.
- *   eps        > 0, finite.
+ *   eps        at least 2^-126, finite.
  *   positions  int64 [T]; not read with rotary_dim 0.
  * The sum of squares and all products are binary32, the result is rounded once:
  * a row whose sum of squares passes 3.4e38 has no meaningful result. */
