@@ -132,9 +132,8 @@ int append(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, i
   a.query_start = query_start;
   a.kv_len = kv_len;
   a.cache = view_of(cache);
-  a.normed = norm != nullptr;
-  a.norm = norm ? *norm : NormWeights{nullptr, nullptr, SV_F32, 1.f, 1.};
-  return to_status(launch_append(a, dtype, cache->dtype, static_cast<hipStream_t>(stream)));
+  if (norm) a.norm = *norm;
+  return to_status((norm ? launch_append_normed : launch_append)(a, dtype, cache->dtype, static_cast<hipStream_t>(stream)));
 }
 
 // Sizes, types and pointers of sv_qk_norm_rope and its backward pass;

@@ -4,85 +4,100 @@
 // A group's requests follow each other, so their new rows do: the rows of a
 // group are taken as one request's over the shared tokens (kShared), each
 // request's rows over its own tokens (kOwn), both by the kernels of
-// sv_attn_kernels.hpp, and a third kernel joins the parts of the two: with a
-// part's maximum m, sum l and weighted values o of row r,
+// sv_attn_kernels.hpp, and a last kernel joins the parts of the two: with a
+// part's maximum m, sum l and weighted values o of a row,
 //   M = max m,  out = sum 2^(m - M) o / sum 2^(m - M) l.
+//
+// The rows of a group are many, which makes the shared part a matter of the
+// matrix units, while a request's own tokens are read for a few rows only and
+// are a matter of HBM: one launch (attn_shared_both.hip) has both at once.
 #include "sv_attn_kernels.hpp"
+#include "sv_attn_shared.hpp"
 
 namespace sv {
 
 namespace {
 
-// Joins the parts of a row's group and of its request.
-template <int M, int ALIGN>
-__global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, SharedPlan p, int per) {
-  __shared__ float4 sums[kAttnThreads];
+// Joins the parts of a row's group and of its request: a wave takes `heads_at`
+// heads of a token in turn, a lane 2 (above 128 channels 4) channels of all
+// parts, whose weights the lanes form, one each, 64 parts at a time.
+template <int M, int ALIGN, int CH>
+__global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, SharedPlan p, int heads_at) {
+  typedef float Some __attribute__((ext_vector_type(CH)));
   const int lane = threadIdx.x & 63;
-  const int G = a.q_heads / a.cache.heads;
-  const int64_t all = int64_t(a.T) * a.q_heads, from = int64_t(blockIdx.x) * per, to = min(from + per, all);
-  // a row's parts: of the group's splits, and of its request's own from the first live one on
-  struct Parts {
-    int shared, own, first;
-  };
-  auto parts_of = [&](int64_t at, auto load) {
-    const int tok = int(at / a.q_heads), head = int(at % a.q_heads);
-    int token0, next;
-    const int b = request_of(a, tok, load, token0, next);
-    if (b < 0) return Parts{-1, 0, 0};
-    Parts out = {0, 0, 0};
-    int before = 0, hi = a.groups, g = 0;  // the last group that starts at b or before is g - 1 in the end
-    while (g < hi) {
-      const int mid = g + ((hi - g) >> 1);
-      if (load(a.group_start, mid) <= b)
-        g = mid + 1;
-      else
-        hi = mid;
-    }
-    if (--g >= 0 && b < load(a.group_start, g + 1)) {
-      before = shared_tokens(a, g, load);
-      if (before > 0) out.shared = min((before - 1) / p.shared.split_len, p.shared.num_splits - 1) + 1;
-    }
+  const int G = a.q_heads / a.cache.heads, D = a.cache.D;
+  const int64_t all = int64_t(a.T) * a.q_heads;
+  const int turns = (a.q_heads + heads_at - 1) / heads_at;  // of waves for a token
+  const int64_t at_wave = int64_t(blockIdx.x) * kAttnWaves + uniform(threadIdx.x >> 6);
+  const int tok = uniform(int(at_wave / turns)), head0 = uniform(int(at_wave % turns)) * heads_at;
+  if (tok >= a.T) return;
+  int token0, next;
+  const int b = request_of(a, tok, uniform_at, token0, next);
+  if (b < 0) return;
+  const int before = shared_tokens_of(a, b);
+  const int shared = before > 0 ? min((before - 1) / p.shared.split_len, p.shared.num_splits - 1) + 1 : 0;
+  const int len = max(uniform_at(a.kv_len, b), 0);
+  const int ch = min(CH * lane, D - CH);
+  for (int head = head0; head < min(head0 + heads_at, a.q_heads); ++head) {
+    const int64_t at = int64_t(tok) * a.q_heads + head;
     const int64_t row = int64_t(tok - token0) * G + head % G;
-    const Tile t = tile_of<M, Part::kOwn, ALIGN>(a, G, token0, int64_t(next) - token0, max(load(a.kv_len, b), 0),
-                                                 row / M * M, before);
-    if (t.rows != 0 && t.begin < t.end) {
-      const Splits live = live_splits(t, p.own.split_len, p.own.num_splits);
-      out.own = live.last - live.first + 1;
-      out.first = p.own.first_part + live.first;
-    }
-    return out;
-  };
-  for (int64_t some = from; some < to; some += 64) {
-    Parts mine = {-1, 0, 0};
-    if (per == 1)
-      mine = parts_of(blockIdx.x, uniform_at);
-    else if (some + lane < to)
-      mine = parts_of(some + lane, [](const int32_t* x, int64_t i) { return x[i]; });
-    for (uint64_t left = __ballot(mine.shared >= 0 && some + lane < to); left != 0; left &= left - 1) {
-      const int k = __builtin_ctzll(left);
-      const int shared = __builtin_amdgcn_readlane(mine.shared, k), own = __builtin_amdgcn_readlane(mine.own, k);
-      const int first = __builtin_amdgcn_readlane(mine.first, k) - shared;
-      const int64_t at = some + k;
-      if (shared + own > 0) {
-        join_row(a, p.own, sums, at, shared + own, [&](int i) { return i < shared ? i : first + i; });
-        continue;
+    const Tile t =
+        tile_of<M, Part::kOwn, ALIGN>(a, G, token0, int64_t(next) - token0, len, row / M * M, before);
+    Splits live = {0, -1};
+    if (t.rows != 0 && t.begin < t.end) live = live_splits(t, p.own.split_len, p.own.num_splits);
+    const int parts = uniform(shared + live.last - live.first + 1), first = uniform(p.own.first_part + live.first - shared);
+    const auto index = [&](int i) { return int64_t(i < shared ? i : first + i) * all + at; };
+    float top = -INFINITY, total = 0.f;
+    Some y = 0.f;
+    for (int from = 0; from < parts; from += 64) {
+      const int n = min(parts - from, 64);
+      // parts are asked for eight at a time, the first ones along with the statistics
+      constexpr int kAhead = 8;
+      Some v[kAhead];
+      const auto ask = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (s + i < n) v[i] = *reinterpret_cast<const Some*>(p.own.part_o + index(from + s + i) * D + ch);
+      };
+      ask(0);
+      const float2 ml = lane < n ? p.own.part_ml[index(from + lane)] : make_float2(-INFINITY, 0.f);
+      float higher = ml.x;
+#pragma unroll
+      for (int i = 32; i >= 1; i >>= 1) higher = fmaxf(higher, __shfl_xor(higher, i, 64));
+      higher = fmaxf(higher, top);
+      const float ref = higher == -INFINITY ? 0.f : higher, keep = fast_exp2(top - ref);
+      top = higher;
+      const float weight = fast_exp2(ml.x - ref);
+      total = fmaf(total, keep, wave_sum(weight * ml.y));
+      y *= keep;
+      for (int s = 0; s < n; s += kAhead) {
+        if (s > 0) ask(s);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (s + i < n) y += v[i] * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), s + i));
       }
-      // a row that sees nothing
-      const int ch = 4 * threadIdx.x;
-      if (ch < a.cache.D)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + at / a.q_heads * a.out.token +
-                                  at % a.q_heads * a.out.head + ch) = make_uint2(0u, 0u);
-      if (a.lse && threadIdx.x == 0) a.lse[at] = -INFINITY;
     }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    if (CH * lane < D) {
+      uint16_t* out = static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + ch;
+#pragma unroll
+      for (int i = 0; i < CH; i += 2) reinterpret_cast<uint32_t*>(out)[i / 2] = pack_bf16(y[i] * inv, y[i + 1] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[at] = total == 0.f ? -INFINITY : (top + fast_log2(total)) * kLn2;
   }
 }
 
 template <int M, int ALIGN>
 void launch_join_shared(const AttnArgs& a, const SharedPlan& p, hipStream_t stream) {
-  const int64_t all = int64_t(a.T) * a.q_heads;
-  const int per = int((all + 4095) / 4096);
-  hipLaunchKernelGGL((join_shared_kernel<M, ALIGN>), dim3(int((all + per - 1) / per)), dim3(kAttnThreads), 0, stream, a,
-                     p, per);
+  // several heads a wave where the waves fill the card all the same
+  const int64_t rows = int64_t(a.T) * a.q_heads;
+  const int heads_at = rows <= 32768 ? 1 : rows <= 131072 ? 4 : 8;
+  const int64_t waves = int64_t(a.T) * ((a.q_heads + heads_at - 1) / heads_at);
+  const dim3 grid(int((waves + kAttnWaves - 1) / kAttnWaves)), block(kAttnThreads);
+  if (a.cache.D <= 128)
+    hipLaunchKernelGGL((join_shared_kernel<M, ALIGN, 2>), grid, block, 0, stream, a, p, heads_at);
+  else
+    hipLaunchKernelGGL((join_shared_kernel<M, ALIGN, 4>), grid, block, 0, stream, a, p, heads_at);
 }
 
 }  // namespace
@@ -101,8 +116,10 @@ SharedPlan plan_shared(int B, int T, int groups, int q_heads, int kv_heads, int 
 }
 
 hipError_t launch_shared(const AttnArgs& a, const SharedPlan& p, int cache_dtype, hipStream_t stream) {
-  launch_part<Part::kShared>(a, p.shared, cache_dtype, stream);
-  launch_part<Part::kOwn>(a, p.own, cache_dtype, stream);
+  if (!launch_shared_and_own(a, p, cache_dtype, stream)) {
+    launch_part<Part::kShared>(a, p.shared, cache_dtype, stream);
+    launch_part<Part::kOwn>(a, p.own, cache_dtype, stream);
+  }
   if (p.own.row_tile == 16)
     launch_join_shared<16, kBlock>(a, p, stream);
   else if (p.own.row_tile == 32)

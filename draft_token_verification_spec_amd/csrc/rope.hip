@@ -46,12 +46,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
   }
 }
 
-// NORM: each query and key head's row is normed before it is turned.
-template <bool VEC, bool FP8, bool NORM, typename ET>
+template <bool VEC, bool FP8, typename ET>
 __global__ __launch_bounds__(kRopeThreads) void append_kernel(AppendArgs a) {
   __shared__ float2 cs[kMaxPairs];
-  __shared__ double2 exact[NORM ? kMaxPairs : 1];
-  __shared__ float w[NORM ? 2 : 1][SV_ATTN_MAX_HEAD_DIM];
   const int t = blockIdx.x;
   // requests of equally many rows are found at once, others by a search
   int b = int(int64_t(t) * a.B / a.T);
@@ -65,17 +62,7 @@ __global__ __launch_bounds__(kRopeThreads) void append_kernel(AppendArgs a) {
   const int place = max(a.kv_len[b], 0) - (end - t);
   const int page = page_of(a.cache, b, place);
   const double position = a.positions ? double(a.positions[t]) : double(place);
-  if constexpr (NORM) {
-    stage_weights(w, a.norm, a.cache.D);
-    for (int i = threadIdx.x; i < a.rotary >> 1; i += kRopeThreads) {
-      double s, c;
-      sincospi(half_turns(position, a.freq[i]), &s, &c);
-      exact[i] = make_double2(c * a.mscale, s * a.mscale);
-      cs[i] = make_float2(float(exact[i].x), float(exact[i].y));
-    }
-  } else {
-    make_angles(cs, a.freq, a.rotary >> 1, position, a.mscale, 1.f);
-  }
+  make_angles(cs, a.freq, a.rotary >> 1, position, a.mscale, 1.f);
   __syncthreads();
 
   const int D = a.cache.D, heads = a.cache.heads;
@@ -87,18 +74,15 @@ __global__ __launch_bounds__(kRopeThreads) void append_kernel(AppendArgs a) {
   for (int g = threadIdx.x >> lg; g < total; g += kRopeThreads >> lg) {
     float y[8] = {};
     if (g < a.q_heads) {
-      const ET* x = static_cast<const ET*>(a.q.p) + int64_t(t) * a.q.token + g * a.q.head;
-      if constexpr (NORM) normed8<VEC>(x, e0, D, a.rotary, a.layout, cs, w[0], a.norm, lanes, y);
       if (!live) continue;
-      if constexpr (!NORM) turned8<VEC>(x, e0, D, a.rotary, a.layout, cs, y);
+      turned8<VEC>(static_cast<const ET*>(a.q.p) + int64_t(t) * a.q.token + g * a.q.head, e0, D, a.rotary, a.layout, cs,
+                   y);
       put8<VEC>(static_cast<ET*>(a.q_out.p) + int64_t(t) * a.q_out.token + g * a.q_out.head, e0, D, y);
     } else if (g < a.q_heads + heads) {
       const int h = g - a.q_heads;
-      const ET* x = static_cast<const ET*>(a.k.p) + int64_t(t) * a.k.token + h * a.k.head;
-      if constexpr (NORM)
-        normed_key8<VEC, FP8>(x, e0, D, a.rotary, a.layout, exact, w[NORM], a.norm, lanes, y);
-      else if (live)
-        turned8<VEC>(x, e0, D, a.rotary, a.layout, cs, y);
+      if (live)
+        turned8<VEC>(static_cast<const ET*>(a.k.p) + int64_t(t) * a.k.token + h * a.k.head, e0, D, a.rotary, a.layout,
+                     cs, y);
       put_cache<FP8>(a.cache, a.cache.k, page * a.cache.k_page + slot * a.cache.k_token + h * a.cache.k_head,
                      a.cache.k_scale, ((int64_t(page) * heads + h) << a.cache.page_shift) + slot, e0, live, y, lanes);
     } else {
@@ -135,17 +119,10 @@ hipError_t launch_rope(const RopeArgs& a, int dtype, hipStream_t stream) {
 template <bool VEC, bool FP8>
 static void append_of(const AppendArgs& a, int dtype, hipStream_t stream) {
   const dim3 grid(a.T), block(kRopeThreads);
-  if (a.normed) {
-    if (dtype == SV_BF16)
-      hipLaunchKernelGGL((append_kernel<VEC, FP8, true, uint16_t>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((append_kernel<VEC, FP8, true, float>), grid, block, 0, stream, a);
-  } else {
-    if (dtype == SV_BF16)
-      hipLaunchKernelGGL((append_kernel<VEC, FP8, false, uint16_t>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((append_kernel<VEC, FP8, false, float>), grid, block, 0, stream, a);
-  }
+  if (dtype == SV_BF16)
+    hipLaunchKernelGGL((append_kernel<VEC, FP8, uint16_t>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((append_kernel<VEC, FP8, float>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream) {

@@ -67,10 +67,10 @@ struct AppendArgs {
   const int32_t* query_start;
   const int32_t* kv_len;
   PagedView cache;
-  bool normed;
-  NormWeights norm;
+  NormWeights norm;  // launch_append_normed
 };
 hipError_t launch_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
+hipError_t launch_append_normed(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
 
 // Pages taken and given back.  scratch: pages_scratch(B, T) bytes (0: none).
 struct PagesArgs {

@@ -91,9 +91,13 @@ __device__ __forceinline__ uint4 load_from(const char* p, uint32_t at) {
 // are therefore turned by 9 places (an XCD and an engine) from head to head, by
 // 27 from split to split: 64 contexts of 1024 to 4096 tokens, shuffled or
 // ascending, 156 and 146 -> 138 us; 4 of 2000 to 60000, 148 -> 84 us.
-__device__ __forceinline__ uint32_t spread_over_xcds(uint32_t x, uint32_t head, uint32_t split) {
-  return (x + 9u * head + 27u * split) % gridDim.x;
+struct Block {
+  uint32_t x, y, z, nx;  // a workgroup's place in its grid, and the grid's width
+};
+__device__ __forceinline__ uint32_t spread_over_xcds(const Block& at) {
+  return (at.x + 9u * at.y + 27u * at.z) % at.nx;
 }
+__device__ __forceinline__ Block this_block() { return {blockIdx.x, blockIdx.y, blockIdx.z, gridDim.x}; }
 
 // Which tokens of its request a row takes.  A tile of rows counts the tokens of
 // its range from `begin` to `end`; in kSinks and kOwn, where the range has a gap,
@@ -298,22 +302,25 @@ constexpr int kValuePitch = DP + 16;
 // SMALL: pages of fewer than 16 tokens (or rows too far apart for a 32-bit
 // offset within 16 tokens): every lane looks its token's page up.  Otherwise 16
 // tokens lie in one page, whose address is scalar.
+template <int DP>
+using FewValues = uint16_t[kAttnWaves][kBlock * kPitch<DP>];
+template <int MT>
+using FewStats = float[kAttnWaves][16 * MT];
+
 template <int DP, int MT, bool FP8, bool SMALL, Part PART>
-__global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 3) void few_rows_kernel(
-    AttnArgs a, AttnPlan p) {
+__device__ __forceinline__ void few_rows(const AttnArgs& a, const AttnPlan& p, FewValues<DP>& values,
+                                         FewStats<MT>& stat_m, FewStats<MT>& stat_l, const Block& block) {
   constexpr int M = 16 * MT;
   constexpr int kSteps = DP / 32;        // of the score product
   constexpr int kDT = DP / 16;           // channel tiles of the result
   constexpr int kLoads = FP8 ? DP / 64 : DP / 32;  // 16-byte loads of a token's row per lane
-  __shared__ __align__(16) uint16_t values[kAttnWaves][kBlock * kPitch<DP>];
-  __shared__ float stat_m[kAttnWaves][M], stat_l[kAttnWaves][M];
 
   const CacheView& c = a.cache;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int kvh = block.y, split = block.z;
   const int G = a.q_heads / c.heads;
-  const int at_x = spread_over_xcds(blockIdx.x, kvh, split);
+  const int at_x = spread_over_xcds(block);
   const int b = at_x / p.tiles;
   for (int64_t first_row = int64_t(at_x - b * p.tiles) * M;; first_row += int64_t(p.tiles) * M) {
     const Tile t = tile_at<M, PART, kBlock>(a, G, b, first_row);
@@ -332,10 +339,7 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
     for (int m = 0; m < MT; ++m) {
       const int row = 16 * m + r;
       const int tok = (t.first_row + row) / G, head = kvh * G + (t.first_row + row) % G;
-      if constexpr (PART == Part::kShared)
-        place[m] = row < t.rows ? place_in_group(a, b, t.token0 + tok) : -1;
-      else
-        place[m] = row < t.rows ? t.place0 + tok : -1;
+      if constexpr (PART != Part::kShared) place[m] = row < t.rows ? t.place0 + tok : -1;
       oldest[m] = PART == Part::kOwn ? t.before - 1 : a.window > 0 ? max(place[m], -1) - a.window : -1;
       const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + int64_t(t.token0 + tok) * a.q.token + head * a.q.head;
 #pragma unroll
@@ -346,13 +350,8 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
       }
     }
     // the places of the tile's first and last rows (kShared: whether some row does not see all)
-    int first_place, last_place = 0;
-    if constexpr (PART == Part::kShared) {
-      bool low = false;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) low |= 16 * m + r < t.rows && place[m] < t.end - 1;
-      first_place = __any(low) ? -1 : INT32_MAX;
-    } else {
+    int first_place = 0, last_place = 0;
+    if constexpr (PART != Part::kShared) {
       first_place = t.place0 + t.first_row / G;
       last_place = t.place0 + (t.first_row + t.rows - 1) / G;
     }
@@ -422,6 +421,16 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
       request_keys(base);
       request_values(base);
       pages(base + stride < end ? base + stride : base);
+      if constexpr (PART == Part::kShared) {  // (looked up while the first keys and values are on their way)
+        bool low = false;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int row = 16 * m + r;
+          place[m] = row < t.rows ? place_in_group(a, b, t.token0 + (t.first_row + row) / G) : -1;
+          low |= row < t.rows && place[m] < t.end - 1;
+        }
+        first_place = __any(low) ? -1 : INT32_MAX;
+      }
       do {
         // the queries are zero beyond the head's channels, but zero times an infinite key would be NaN
         if (c.D < DP) {
@@ -653,6 +662,14 @@ __global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 
   }
 }
 
+template <int DP, int MT, bool FP8, bool SMALL, Part PART>
+__global__ __launch_bounds__(kAttnThreads, DP == 256 ? 1 : DP * MT >= 128 ? 2 : 3) void few_rows_kernel(
+    AttnArgs a, AttnPlan p) {
+  __shared__ __align__(16) FewValues<DP> values;
+  __shared__ FewStats<MT> stat_m, stat_l;
+  few_rows<DP, MT, FP8, SMALL, PART>(a, p, values, stat_m, stat_l, this_block());
+}
+
 // ---------------------------------------------------------------------------
 // many rows
 // ---------------------------------------------------------------------------
@@ -670,9 +687,17 @@ constexpr int kManyRows = 32 * kAttnWaves;
 // PAGES: 0 pages of fewer than 16 tokens (or rows too far apart for a 32-bit
 // offset), every thread looks its tokens' pages up; 1 a load's tokens of a wave
 // lie in one page; 2 the tile lies in one page.
+template <int DP>
+using ManyKeys = uint16_t[2][kTile * kPitch<DP>];
+template <int DP>
+using ManyValues = uint16_t[2][kTile * kValuePitch<DP>];
+using ManyState = uint8_t[2][kTile];    // of a token: 0 present, 1 absent, 2 a value not finite
+using ManyMarks = int[2][kAttnWaves];   // some token that this wave loaded has a state
+
 template <int DP, bool FP8, int PAGES, Part PART>
-__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void many_rows_kernel(
-    AttnArgs a, AttnPlan p) {
+__device__ __forceinline__ void many_rows(const AttnArgs& a, const AttnPlan& p, ManyKeys<DP>& keys,
+                                          ManyValues<DP>& values, ManyState& state, ManyMarks& marks,
+                                          const Block& block) {
   constexpr int M = kManyRows;
   constexpr int kSteps = DP / 16;
   constexpr int kDT = DP / 32;
@@ -682,26 +707,22 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
   constexpr int kLoads = kTile / kSpan;
   constexpr int kParts = FP8 ? 2 : 1;             // 8 channels each, of a load
   constexpr int kGroup = DP == 64 ? 2 : 4;        // products whose operands are read together
-  __shared__ __align__(16) uint16_t keys[2][kTile * kPitch<DP>];
-  __shared__ __align__(16) uint16_t values[2][kTile * kValuePitch<DP>];
-  __shared__ __align__(16) uint8_t state[2][kTile];   // of a token: 0 present, 1 absent, 2 a value not finite
-  __shared__ __align__(16) int marks[2][kAttnWaves];  // some token that this wave loaded has a state
 
   const CacheView& c = a.cache;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int split = blockIdx.z;
+  const int split = block.z;
   const int G = a.q_heads / c.heads;
   // workgroups go to the 8 XCDs in turn: each takes whole heads, whose keys and
   // values then pass through one L2 only
-  uint32_t at_x = blockIdx.x, kvh = blockIdx.y;
+  uint32_t at_x = block.x, kvh = block.y;
   if ((c.heads & 7) == 0) {
-    const uint32_t i = blockIdx.x + blockIdx.y * gridDim.x, per = gridDim.x * (c.heads >> 3);
+    const uint32_t i = block.x + block.y * block.nx, per = block.nx * (c.heads >> 3);
     const uint32_t pos = (i & 7) * per + (i >> 3);
-    kvh = pos / gridDim.x;
-    at_x = pos - kvh * gridDim.x;
+    kvh = pos / block.nx;
+    at_x = pos - kvh * block.nx;
   } else {
-    at_x = spread_over_xcds(blockIdx.x, kvh, split);
+    at_x = spread_over_xcds(block);
   }
   const int b = at_x / p.tiles;
   // later tiles of a prompt see more: they start first
@@ -1068,6 +1089,16 @@ __global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void 
   }
 }
 
+template <int DP, bool FP8, int PAGES, Part PART>
+__global__ __launch_bounds__(kAttnThreads, DP > 128 ? 1 : DP > 64 ? 2 : 3) void many_rows_kernel(
+    AttnArgs a, AttnPlan p) {
+  __shared__ __align__(16) ManyKeys<DP> keys;
+  __shared__ __align__(16) ManyValues<DP> values;
+  __shared__ __align__(16) ManyState state;
+  __shared__ __align__(16) ManyMarks marks;
+  many_rows<DP, FP8, PAGES, PART>(a, p, keys, values, state, marks, this_block());
+}
+
 // ---------------------------------------------------------------------------
 // joining splits
 // ---------------------------------------------------------------------------
@@ -1238,10 +1269,15 @@ void launch_dims(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     launch_rows<256, FP8, SMALL, PART>(a, p, stream);
 }
 
+// Whether 16 tokens may lie in several pages, or farther apart than 2^32 bytes.
+bool looks_up_each_token(const CacheView& c) {
+  const auto near = [](const UnitStrides& u) { return u.token < (uint32_t(1) << 24); };
+  return c.page_shift < 4 || !near(c.ku) || !near(c.vu);
+}
+
 template <Part PART>
 void launch_part(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream) {
-  const auto near = [](const UnitStrides& u) { return u.token < (uint32_t(1) << 24); };  // 16 tokens within 2^32 bytes
-  const bool small = a.cache.page_shift < 4 || !near(a.cache.ku) || !near(a.cache.vu);
+  const bool small = looks_up_each_token(a.cache);
   if (cache_dtype == SV_E4M3)
     small ? launch_dims<true, true, PART>(a, p, stream) : launch_dims<true, false, PART>(a, p, stream);
   else

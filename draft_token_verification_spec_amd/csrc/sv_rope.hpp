@@ -1,5 +1,5 @@
 // Shared by the kernels that turn heads' rows: angles, rows of 8 channels a
-// lane, norms of rows, and their way into a cache.
+// lane, and their way into a cache.
 #pragma once
 
 #include "sv_attn.hpp"
@@ -94,161 +94,6 @@ __device__ __forceinline__ void put8(ET* out, int e0, int D, const float (&y)[8]
 
 // log2 of the lanes that take a head.
 __host__ __device__ inline int head_lanes_log2(int D) { return D <= 64 ? 3 : D <= 128 ? 4 : 5; }
-
-// The weights of queries' and keys' norms, to LDS as floats (none: ones), by the
-// whole workgroup.
-__device__ __forceinline__ void stage_weights(float (*w)[SV_ATTN_MAX_HEAD_DIM], const NormWeights& n, int D) {
-  for (int i = threadIdx.x; i < 2 * D; i += kRopeThreads) {
-    const int k = i >= D, e = k ? i - D : i;
-    const void* p = k ? n.k : n.q;
-    w[k][e] = !p ? 1.f : n.dtype == SV_BF16 ? load1(static_cast<const uint16_t*>(p) + e) : load1(static_cast<const float*>(p) + e);
-  }
-}
-
-// The sum over a group of `lanes` lanes, in each of them.
-__device__ __forceinline__ float group_sum(float x, int lanes) {
-  for (int o = lanes >> 1; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
-  return x;
-}
-
-// (mean of squares + eps)^-1/2 of a row whose 8 channels a lane are y (zeros
-// beyond the row).  The squares are summed pairwise in binary32; what follows is
-// one step of Newton's method in binary64, five operations, so that the result
-// adds no more than its own rounding to the sum's.
-__device__ __forceinline__ float inverse_norm(const float (&y)[8], const NormWeights& n, int lanes) {
-  const auto two = [&](int j) { return fmaf(y[j], y[j], y[j + 1] * y[j + 1]); };
-  const float sq = (two(0) + two(2)) + (two(4) + two(6));
-  const double m = double(group_sum(sq, lanes)) * n.inv_dim + n.eps;
-  const double r = __builtin_amdgcn_rsqf(float(m));
-  return float(r * (1.5 - 0.5 * m * r * r));
-}
-
-// The row's channels e0 .. e0 + 7 (zeros beyond it) and those that they are
-// paired with (of turned channels; SV_ROPE_INTERLEAVED with VEC: not written,
-// the pairs lie in y).
-template <bool VEC, typename ET>
-__device__ __forceinline__ void load_pairs8(const ET* x, int e0, int D, int rotary, int layout, float (&y)[8],
-                                            float (&z)[8]) {
-  const int half = rotary >> 1;
-  if (VEC) {
-    if (e0 >= D) return;
-    load8(x + e0, y);
-    if (e0 < rotary && layout == SV_ROPE_HALF) load8(x + (e0 < half ? e0 + half : e0 - half), z);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = e0 + j;
-      if (e >= D) continue;
-      y[j] = load1(x + e);
-      if (e < rotary) z[j] = load1(x + (layout == SV_ROPE_HALF ? (e < half ? e + half : e - half) : e ^ 1));
-    }
-  }
-}
-
-// y, with what it is paired with in z, times the weights, turned, and times r:
-// in this order the first product is exact for bf16 rows and weights, and the
-// row's sum is needed last.  (Explicitly fused, so that a row's bits do not depend
-// on its alignment.)
-template <bool VEC>
-__device__ __forceinline__ void normed_and_turned8(float (&y)[8], float (&z)[8], int e0, int D, int rotary, int layout,
-                                                   const float2* cs, const float* w, float r) {
-  const int half = rotary >> 1;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (VEC || e0 + j < D) y[j] *= w[e0 + j];
-  if (VEC) {
-    if (e0 < rotary) {
-      if (layout == SV_ROPE_HALF) {
-        const bool first = e0 < half;
-        const int i0 = first ? e0 : e0 - half, o0 = first ? e0 + half : i0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 t = cs[i0 + j];
-          z[j] *= w[o0 + j];
-          y[j] = fmaf(y[j], t.x, first ? -(z[j] * t.y) : z[j] * t.y);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float2 t = cs[(e0 + j) >> 1];
-          const float a = y[j], c = y[j + 1];
-          y[j] = fmaf(a, t.x, -(c * t.y));
-          y[j + 1] = fmaf(c, t.x, a * t.y);
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = e0 + j;
-      if (e >= D || e >= rotary) continue;
-      const bool first = layout == SV_ROPE_HALF ? e < half : (e & 1) == 0;
-      const int other = layout == SV_ROPE_HALF ? (first ? e + half : e - half) : e ^ 1;
-      const float2 t = cs[layout == SV_ROPE_HALF ? (first ? e : other) : e >> 1];
-      z[j] *= w[other];
-      y[j] = fmaf(y[j], t.x, first ? -(z[j] * t.y) : z[j] * t.y);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] *= r;
-}
-
-// One head's row x normed and turned, by all lanes of its group.
-template <bool VEC, typename ET>
-__device__ __forceinline__ void normed8(const ET* x, int e0, int D, int rotary, int layout, const float2* cs,
-                                        const float* w, const NormWeights& n, int lanes, float (&y)[8]) {
-  float z[8] = {};
-  load_pairs8<VEC>(x, e0, D, rotary, layout, y, z);
-  const float r = inverse_norm(y, n, lanes);
-  if (e0 < D) normed_and_turned8<VEC>(y, z, e0, D, rotary, layout, cs, w, r);
-}
-
-// A number that rounds to e4m3 as x does: x without what binary32 has no place
-// for, its last bit set where something is missing.  (Beyond binary32's normal
-// numbers: the nearest one.)
-__device__ __forceinline__ float shortened(double x) {
-  const uint64_t bits = __double_as_longlong(x);
-  const uint32_t high = uint32_t(bits >> 32), low = uint32_t(bits);
-  const uint32_t size = high & 0x7fffffffu;
-  if (size - (897u << 20) >= 253u << 20) return float(x);
-  return __uint_as_float((high & 0x80000000u) | ((size - (896u << 20)) << 3) | (low >> 29) | ((low & 0x1fffffffu) != 0));
-}
-
-// One head's row x normed and turned in binary64, by all lanes of its group:
-// keys, which are stored once and read by every later row, are so the nearest
-// 8-bit values (FP8; in binary32 some 10^-6 of them are not), or the nearest
-// binary32 ones on their way to bf16.  cs: binary64 too.
-template <bool VEC, bool FP8, typename ET>
-__device__ __forceinline__ void normed_key8(const ET* x, int e0, int D, int rotary, int layout, const double2* cs,
-                                            const float* w, const NormWeights& n, int lanes, float (&y)[8]) {
-  float z[8] = {};
-  load_pairs8<VEC>(x, e0, D, rotary, layout, y, z);
-  if (VEC && layout == SV_ROPE_INTERLEAVED) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = y[j ^ 1];
-  }
-  double sq = 0.;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sq = fma(double(y[j]), double(y[j]), sq);
-  for (int o = lanes >> 1; o >= 1; o >>= 1) sq += __shfl_xor(sq, o, 64);
-  const double m = sq * n.inv_dim + n.eps, near = __builtin_amdgcn_rsqf(float(m));
-  const double r = near * (1.5 - 0.5 * m * near * near);
-  const int half = rotary >> 1;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = e0 + j;
-    if (e >= D) continue;
-    double v = double(y[j]) * w[e];
-    if (e < rotary) {
-      const bool first = layout == SV_ROPE_HALF ? e < half : (e & 1) == 0;
-      const int other = layout == SV_ROPE_HALF ? (first ? e + half : e - half) : e ^ 1;
-      const double2 t = cs[layout == SV_ROPE_HALF ? (first ? e : other) : e >> 1];
-      const double u = double(z[j]) * w[other] * t.y;
-      v = fma(v, t.x, first ? -u : u);
-    }
-    y[j] = FP8 ? shortened(v * r) : float(v * r);
-  }
-}
 
 // Least e >= -117 with amax <= 448 * 2^e: 448 = 0.875 * 2^9 (-9 for 0).  The
 // type's smallest step, 2^-9, times 2^-117 is still a normal bf16 value.
