@@ -18,6 +18,32 @@ namespace sv {
 
 namespace {
 
+// The parts of a request's rows, as the kernels that wrote them saw them: those
+// of the group's splits, and of its own live ones.
+template <int M, int ALIGN>
+struct PartsOf {
+  const AttnArgs& a;
+  const SharedPlan& p;
+  int token0, next, len, before, shared;
+  __device__ __forceinline__ PartsOf(const AttnArgs& a, const SharedPlan& p, int b, int token0, int next)
+      : a(a), p(p), token0(token0), next(next) {
+    len = max(uniform_at(a.kv_len, b), 0);
+    before = shared_tokens_of(a, b);
+    shared = before > 0 ? min((before - 1) / p.shared.split_len, p.shared.num_splits - 1) + 1 : 0;
+  }
+  // The i-th of a row's `parts` parts is the call's i-th (i < shared) or (first + i)-th.
+  __device__ __forceinline__ void of(int tok, int head, int& parts, int& first) const {
+    const int G = a.q_heads / a.cache.heads;
+    const int64_t row = int64_t(tok - token0) * G + head % G;
+    const Tile t =
+        tile_of<M, Part::kOwn, ALIGN>(a, G, token0, int64_t(next) - token0, len, row / M * M, before);
+    Splits live = {0, -1};
+    if (t.rows != 0 && t.begin < t.end) live = live_splits(t, p.own.split_len, p.own.num_splits);
+    parts = uniform(shared + live.last - live.first + 1);
+    first = uniform(p.own.first_part + live.first - shared);
+  }
+};
+
 // Joins the parts of a row's group and of its request: a wave takes `heads_at`
 // heads of a token in turn, a lane 2 (above 128 channels 4) channels of all
 // parts, whose weights the lanes form, one each, 64 parts at a time.
@@ -25,7 +51,7 @@ template <int M, int ALIGN, int CH>
 __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, SharedPlan p, int heads_at) {
   typedef float Some __attribute__((ext_vector_type(CH)));
   const int lane = threadIdx.x & 63;
-  const int G = a.q_heads / a.cache.heads, D = a.cache.D;
+  const int D = a.cache.D;
   const int64_t all = int64_t(a.T) * a.q_heads;
   const int turns = (a.q_heads + heads_at - 1) / heads_at;  // of waves for a token
   const int64_t at_wave = int64_t(blockIdx.x) * kAttnWaves + uniform(threadIdx.x >> 6);
@@ -34,19 +60,13 @@ __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, S
   int token0, next;
   const int b = request_of(a, tok, uniform_at, token0, next);
   if (b < 0) return;
-  const int before = shared_tokens_of(a, b);
-  const int shared = before > 0 ? min((before - 1) / p.shared.split_len, p.shared.num_splits - 1) + 1 : 0;
-  const int len = max(uniform_at(a.kv_len, b), 0);
+  const PartsOf<M, ALIGN> rows(a, p, b, token0, next);
   const int ch = min(CH * lane, D - CH);
   for (int head = head0; head < min(head0 + heads_at, a.q_heads); ++head) {
     const int64_t at = int64_t(tok) * a.q_heads + head;
-    const int64_t row = int64_t(tok - token0) * G + head % G;
-    const Tile t =
-        tile_of<M, Part::kOwn, ALIGN>(a, G, token0, int64_t(next) - token0, len, row / M * M, before);
-    Splits live = {0, -1};
-    if (t.rows != 0 && t.begin < t.end) live = live_splits(t, p.own.split_len, p.own.num_splits);
-    const int parts = uniform(shared + live.last - live.first + 1), first = uniform(p.own.first_part + live.first - shared);
-    const auto index = [&](int i) { return int64_t(i < shared ? i : first + i) * all + at; };
+    int parts, first;
+    rows.of(tok, head, parts, first);
+    const auto index = [&](int i) { return int64_t(i < rows.shared ? i : first + i) * all + at; };
     float top = -INFINITY, total = 0.f;
     Some y = 0.f;
     for (int from = 0; from < parts; from += 64) {
@@ -87,10 +107,39 @@ __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, S
   }
 }
 
+// The same for few rows of many parts: a workgroup a row.
+template <int M, int ALIGN>
+__global__ __launch_bounds__(kAttnThreads) void join_few_shared_kernel(AttnArgs a, SharedPlan p) {
+  __shared__ float4 sums[kAttnThreads];
+  const int tok = blockIdx.x, head = blockIdx.y;
+  int token0, next;
+  const int b = request_of(a, tok, uniform_at, token0, next);
+  if (b < 0) return;
+  const PartsOf<M, ALIGN> row(a, p, b, token0, next);
+  int parts, first;
+  row.of(tok, head, parts, first);
+  const int64_t at = int64_t(tok) * a.q_heads + head;
+  if (parts > 0) {
+    join_row(a, p.own, sums, at, parts, [&](int i) { return i < row.shared ? i : first + i; });
+    return;
+  }
+  // a row that sees nothing
+  const int ch = 4 * threadIdx.x;
+  if (ch < a.cache.D)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + int64_t(tok) * a.out.token + head * a.out.head + ch) =
+        make_uint2(0u, 0u);
+  if (a.lse && threadIdx.x == 0) a.lse[at] = -INFINITY;
+}
+
 template <int M, int ALIGN>
 void launch_join_shared(const AttnArgs& a, const SharedPlan& p, hipStream_t stream) {
-  // several heads a wave where the waves fill the card all the same
   const int64_t rows = int64_t(a.T) * a.q_heads;
+  // (8 requests of 32 heads with 64 parts: 6 us, a wave a row 11)
+  if (rows <= 1024 && p.shared.num_splits + p.own.num_splits > 16) {
+    hipLaunchKernelGGL((join_few_shared_kernel<M, ALIGN>), dim3(a.T, a.q_heads), dim3(kAttnThreads), 0, stream, a, p);
+    return;
+  }
+  // several heads a wave where the waves fill the card all the same
   const int heads_at = rows <= 32768 ? 1 : rows <= 131072 ? 4 : 8;
   const int64_t waves = int64_t(a.T) * ((a.q_heads + heads_at - 1) / heads_at);
   const dim3 grid(int((waves + kAttnWaves - 1) / kAttnWaves)), block(kAttnThreads);
@@ -106,6 +155,21 @@ SharedPlan plan_shared(int B, int T, int groups, int q_heads, int kv_heads, int 
                        int max_shared_len, int max_own_len) {
   SharedPlan p;
   p.shared = plan_attention(groups, T, q_heads, kv_heads, D, max_group_len, max_shared_len);
+  if (p.shared.row_tile > 32) {
+    // A workgroup a compute unit, as far as 256 tokens for each go: the own
+    // parts' take the other places, and every split is a part to be written and
+    // read (128 requests behind 8000: two a compute unit 74 + 10 us, one 66 + 8,
+    // one for two 76 + 7).
+    const int64_t tiles = int64_t(groups) * p.shared.tiles * kv_heads;
+    int64_t n = tiles > 0 ? (256 + tiles - 1) / tiles : 1;
+    const int64_t most = (int64_t(max_shared_len) + 255) / 256;
+    n = n < most ? n : most;
+    if (n < p.shared.num_splits) {
+      const int64_t len = n > 1 ? ((max_shared_len + n - 1) / n + 127) / 128 * 128 : max_shared_len;
+      p.shared.split_len = int(len < 128 ? 128 : len);
+      p.shared.num_splits = n > 1 ? int((int64_t(max_shared_len) + p.shared.split_len - 1) / p.shared.split_len) : 1;
+    }
+  }
   p.own = plan_attention(B, T, q_heads, kv_heads, D, max_q_len, max_own_len);
   p.own.first_part = p.shared.num_splits;
   const size_t rows = size_t(T) * q_heads, parts = size_t(p.shared.num_splits) + p.own.num_splits;

@@ -1,10 +1,10 @@
 // The shared and the own part of attention behind shared tokens in one launch
 // (attn_shared.hip joins their parts).
 //
-// Workgroups of the two alternate: the dispatcher deals them to the 8 XCDs in
-// turn, so eight of one kind follow eight of the other, and within an XCD to its
-// 32 compute units in turn, so the order of the two is exchanged every 32
-// eights, that a compute unit holds both.
+// Those of the shared part, which take longer, come first.  (Eight of either kind
+// in turn, which has both on every compute unit from the start, take as long or a
+// little longer: 128 requests behind 8000 tokens 66 and 67 us, verification of 256
+// behind 8 prompts 250 and 252.)
 #include "sv_attn_kernels.hpp"
 #include "sv_attn_shared.hpp"
 
@@ -34,19 +34,13 @@ struct ManyLds {
 // S, O: tiles of 16 rows of the shared and of the own part; S == 0: 128 rows.
 template <int DP, bool FP8, int PAGES, int S, int O>
 __global__ __launch_bounds__(kAttnThreads, DP > 64 ? 2 : 3) void shared_and_own_kernel(
-    AttnArgs a, SharedPlan p, uint32_t shared_groups, uint32_t own_groups) {
+    AttnArgs a, SharedPlan p, uint32_t shared_blocks) {
   constexpr int kSharedLds = S == 0 ? int(sizeof(ManyLds<DP>)) : int(sizeof(FewLds<DP, S ? S : 1>));
   constexpr int kOwnLds = int(sizeof(FewLds<DP, O>));
   __shared__ __align__(16) char lds[kSharedLds > kOwnLds ? kSharedLds : kOwnLds];
-  // the j-th eight: of either kind in turn while both last
-  const uint32_t j = blockIdx.x >> 3, both = min(shared_groups, own_groups);
-  bool own = own_groups > shared_groups;
-  uint32_t at = j - both;
-  if (j < 2 * both) {
-    own = ((j ^ (j >> 5)) & 1) != 0;
-    at = j >> 1;
-  }
-  const uint32_t i = 8 * at + (blockIdx.x & 7), heads = a.cache.heads;
+  // (either kind's number is rounded up to the XCDs', so that both are dealt to them alike)
+  const bool own = blockIdx.x >= shared_blocks;
+  const uint32_t i = own ? blockIdx.x - shared_blocks : blockIdx.x, heads = a.cache.heads;
   if (own) {
     const uint32_t nx = a.B * p.own.tiles;
     if (i >= nx * heads * p.own.num_splits) return;
@@ -67,10 +61,12 @@ __global__ __launch_bounds__(kAttnThreads, DP > 64 ? 2 : 3) void shared_and_own_
 
 template <int DP, bool FP8, int PAGES, int S, int O>
 void launch_both(const AttnArgs& a, const SharedPlan& p, hipStream_t stream) {
-  const auto eights = [&](int64_t n, const AttnPlan& q) { return uint32_t((n * q.tiles * a.cache.heads * q.num_splits + 7) / 8); };
-  const uint32_t shared = eights(a.groups, p.shared), own = eights(a.B, p.own);
-  hipLaunchKernelGGL((shared_and_own_kernel<DP, FP8, PAGES, S, O>), dim3(8 * (shared + own)), dim3(kAttnThreads), 0, stream,
-                     a, p, shared, own);
+  const auto blocks = [&](int64_t n, const AttnPlan& q) {
+    return uint32_t((n * q.tiles * a.cache.heads * q.num_splits + 7) / 8 * 8);
+  };
+  const uint32_t shared = blocks(a.groups, p.shared), own = blocks(a.B, p.own);
+  hipLaunchKernelGGL((shared_and_own_kernel<DP, FP8, PAGES, S, O>), dim3(shared + own), dim3(kAttnThreads), 0, stream, a, p,
+                     shared);
 }
 
 template <int DP, bool FP8, int O>

@@ -134,9 +134,14 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs& a, int g, Load load
 }
 
 // The tokens that request b shares: those of the group that it is in, if any.
-// The group is found by the whole wave.
+// Groups of equally many requests are found at once, others by a search of the
+// whole wave.
 __device__ __forceinline__ int shared_tokens_of(const AttnArgs& a, int b) {
-  const int g = uniform(find_sequence(a.group_start, a.groups, b, threadIdx.x & 63));
+  int g = int(int64_t(b) * a.groups / a.B);
+  const int first = uniform_at(a.group_start, g), next = uniform_at(a.group_start, g + 1);
+  const int shared = shared_tokens(a, g, uniform_at);
+  if (b >= first && b < next) return shared;
+  g = uniform(find_sequence(a.group_start, a.groups, b, threadIdx.x & 63));
   if (g < 0 || b >= uniform_at(a.group_start, g + 1)) return 0;
   return shared_tokens(a, g, uniform_at);
 }
