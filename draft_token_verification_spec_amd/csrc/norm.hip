@@ -420,11 +420,13 @@ __device__ __forceinline__ void norm_and_turn_key8(float (&y)[8], const float (&
   for (int j = 0; j < 8; ++j) y[j] = FP8 ? shortened(u[j] * r) : float(u[j] * r);
 }
 
-// One workgroup per row, as rope.hip's append.  (Measured on 8285 binary32 rows
-// of 32 + 8 + 8 heads of 128 into an 8-bit cache: four rows a workgroup, or a
-// head's channels asked for ahead, cost registers and so waves: XX us.)
+// One workgroup per row, as rope.hip's append.  Bound by HBM for many rows: 8285
+// binary32 rows of 32 + 8 + 8 heads of 128 into an 8-bit cache, 357 MB in 75 us
+// (4.8 TB/s); by latency for few: 1280 bf16 rows of the same heads 12.5 us.  Four
+// rows a workgroup, or a head's channels asked for ahead, cost registers and so
+// waves (85 to 98 us, 13 to 16).
 template <int LG, bool VEC, bool FP8, typename ET>
-__global__ __launch_bounds__(kRopeThreads) void append_normed_kernel(AppendArgs a) {
+__global__ __launch_bounds__(kRopeThreads, VEC ? 5 : 4) void append_normed_kernel(AppendArgs a) {
   __shared__ float2 cs[kMaxPairs];
   __shared__ double2 exact[kMaxPairs];
   __shared__ Weights w;

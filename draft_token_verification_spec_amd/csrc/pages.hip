@@ -13,8 +13,9 @@
 // Bound by latency: a scan and three dependent copies.  Up to 1024 requests
 // and kSmallRows rows one workgroup does it all, the copies shared evenly over
 // its threads, each of which finds its item's request by a search in LDS.
-// Otherwise three launches: the scan, the pages given back, and the pages taken
-// with the slots, the latter two by workgroups of one request each.
+// Otherwise two launches: the sums with the pages given back, by up to 256
+// workgroups, each of which adds up all requests for itself, and the pages taken
+// with the slots, by workgroups of one request each.
 #include "sv_attn.hpp"
 
 namespace sv {
@@ -45,9 +46,24 @@ __device__ __forceinline__ int64_t pages_on_stack(const PagesArgs& a) {
   return min(max(*a.free_count, 0), a.num_pages);
 }
 
-// Exclusive sums over the workgroup of two numbers per thread; `total` gets the
-// sums.  Ends with every thread past its reads of `waves`.
-__device__ __forceinline__ longlong2 scan_pairs(longlong2 x, longlong2 (&waves)[kPagesThreads / 64], longlong2& total) {
+__device__ __forceinline__ int64_t wave_total(int64_t x) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(static_cast<long long>(x), o, 64);
+  return x;
+}
+
+// Exclusive sums over the workgroup of two numbers per thread, and the sums of
+// these and of three more over all threads.
+struct Sums {
+  longlong2 before, total;
+  int64_t more[3];
+};
+struct SumsLds {
+  longlong2 pairs[kPagesThreads / 64];
+  int64_t more[3][kPagesThreads / 64];
+};
+template <int MORE>
+__device__ __forceinline__ Sums sum_up(longlong2 x, const int64_t (&more)[3], SumsLds& lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   longlong2 upto = x;
 #pragma unroll
@@ -55,29 +71,57 @@ __device__ __forceinline__ longlong2 scan_pairs(longlong2 x, longlong2 (&waves)[
     const int64_t p = __shfl_up(static_cast<long long>(upto.x), o, 64), q = __shfl_up(static_cast<long long>(upto.y), o, 64);
     if (lane >= o) upto.x += p, upto.y += q;
   }
-  if (lane == 63) waves[wave] = upto;
-  __syncthreads();
-  longlong2 before = {0, 0};
-  total = {0, 0};
-  for (int w = 0; w < kPagesThreads / 64; ++w) {
-    if (w < wave) before.x += waves[w].x, before.y += waves[w].y;
-    total.x += waves[w].x, total.y += waves[w].y;
+  if (lane == 63) lds.pairs[wave] = upto;
+#pragma unroll
+  for (int i = 0; i < MORE; ++i) {
+    const int64_t t = wave_total(more[i]);
+    if (lane == 0) lds.more[i][wave] = t;
   }
   __syncthreads();
-  return {before.x + upto.x - x.x, before.y + upto.y - x.y};
+  Sums s = {{upto.x - x.x, upto.y - x.y}, {0, 0}, {0, 0, 0}};
+  for (int w = 0; w < kPagesThreads / 64; ++w) {
+    const longlong2 p = lds.pairs[w];
+    if (w < wave) s.before.x += p.x, s.before.y += p.y;
+    s.total.x += p.x, s.total.y += p.y;
+#pragma unroll
+    for (int i = 0; i < MORE; ++i) s.more[i] += lds.more[i][w];
+  }
+  return s;
 }
 
 // The last of n ascending entries that is at most x (the first is).
 template <typename E, typename X>
 __device__ __forceinline__ int last_upto(const E* v, int n, X x) {
   int lo = 0;
-  for (int step = 512; step > 0; step >>= 1)
+  for (int step = n <= 64 ? 32 : 512; step > 0; step >>= 1)
     if (lo + step < n && v[lo + step] <= x) lo += step;
   return lo;
 }
 
-__device__ __forceinline__ void put_on_stack(const PagesArgs& a, int64_t at, int page) {
-  if (at >= 0 && at < a.num_pages) a.free_pages[at] = page;
+// The workgroup's pages given back: the k-th of `total`, of the last request r of
+// n with from[r] <= k, to place top - k of the stack.  Four a thread at a time.
+__device__ __forceinline__ void give_back(const PagesArgs& a, int b0, int n, const int64_t* from, const int* need,
+                                          int64_t total, int64_t top) {
+  constexpr int kAtATime = 4;
+  for (int64_t k0 = threadIdx.x; k0 < total; k0 += kAtATime * kPagesThreads) {
+    int32_t* entry[kAtATime];
+    int page[kAtATime];
+#pragma unroll
+    for (int i = 0; i < kAtATime; ++i) {
+      const int64_t k = min(k0 + i * kPagesThreads, total - 1);
+      const int r = last_upto(from, n, k);
+      entry[i] = a.table + (b0 + r) * a.table_stride + need[r] + (k - from[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtATime; ++i) page[i] = *entry[i];
+#pragma unroll
+    for (int i = 0; i < kAtATime; ++i) {
+      const int64_t k = k0 + i * kPagesThreads, at = top - k;
+      if (k >= total) break;
+      if (at >= 0 && at < a.num_pages) a.free_pages[at] = page[i];
+      *entry[i] = -1;
+    }
+  }
 }
 
 // The slot of a row at `place` of a request that holds `held` pages, of which
@@ -95,7 +139,7 @@ __device__ __forceinline__ void put_row(const PagesArgs& a, int t, int b, int64_
 }
 
 __global__ __launch_bounds__(kPagesThreads) void pages_small_kernel(PagesArgs a) {
-  __shared__ longlong2 waves[kPagesThreads / 64];
+  __shared__ SumsLds lds;
   __shared__ int64_t give_from[kPagesThreads], take_from[kPagesThreads];
   __shared__ int old[kPagesThreads], now[kPagesThreads], start[kPagesThreads + 1], length[kPagesThreads];
   const int b = threadIdx.x;
@@ -108,8 +152,8 @@ __global__ __launch_bounds__(kPagesThreads) void pages_small_kernel(PagesArgs a)
   if (a.query_start)
     for (int i = b; i <= a.B; i += kPagesThreads) start[i] = a.query_start[i];
   const int64_t count0 = pages_on_stack(a);
-  longlong2 total;
-  const longlong2 from = scan_pairs({c.give(), c.take()}, waves, total);
+  const Sums sums = sum_up<0>({c.give(), c.take()}, {0, 0, 0}, lds);
+  const longlong2 from = sums.before, total = sums.total;
   const int64_t count = min(count0 + total.x, int64_t(a.num_pages));
   const int64_t upto = from.y + c.take();
   const bool granted = c.fits && (c.take() == 0 || upto <= count);
@@ -122,12 +166,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_small_kernel(PagesArgs a)
   __syncthreads();  // (all have read the count)
   const bool crosses = live && upto > count && from.y <= count;  // the first request that is refused
   if (crosses || (b == a.B - 1 && upto <= count)) *a.free_count = int(count - (crosses ? from.y : upto));
-  for (int64_t k = b; k < total.x; k += kPagesThreads) {
-    const int r = last_upto(give_from, a.B, k);
-    int32_t* const entry = a.table + r * a.table_stride + now[r] + (k - give_from[r]);
-    put_on_stack(a, count0 + total.x - 1 - k, *entry);
-    *entry = -1;
-  }
+  give_back(a, 0, a.B, give_from, now, total.x, count0 + total.x - 1);
   __syncthreads();
   for (int64_t k = b; k < min(total.y, count); k += kPagesThreads) {
     const int r = last_upto(take_from, a.B, k);
@@ -143,44 +182,39 @@ __global__ __launch_bounds__(kPagesThreads) void pages_small_kernel(PagesArgs a)
   }
 }
 
-// What a scan leaves for the copies: [B] pairs of exclusive sums, the pages on
-// the stack before and after what is given back, [B] pages held before.
+// What the first launch leaves for the second: the pages on the stack after what
+// is given back, [B] pairs of exclusive sums, [B] pages held before.
 __device__ __forceinline__ longlong2* sums_of(const PagesArgs& a) { return static_cast<longlong2*>(a.scratch) + 1; }
 __device__ __forceinline__ int32_t* held_of(const PagesArgs& a) { return reinterpret_cast<int32_t*>(sums_of(a) + a.B); }
 
-__global__ __launch_bounds__(kPagesThreads) void pages_scan_kernel(PagesArgs a) {
-  __shared__ longlong2 waves[kPagesThreads / 64];
-  longlong2 carry = {0, 0};
-  int held = int(threadIdx.x) < a.B ? a.held[threadIdx.x] : 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
-    const int b = b0 + threadIdx.x;
-    Change c = {0, 0, true};
-    if (b < a.B) c = change_of(a, b, held);
-    if (b + kPagesThreads < a.B) held = a.held[b + kPagesThreads];
-    longlong2 total;
-    const longlong2 from = scan_pairs({c.give(), c.take()}, waves, total);
-    if (b < a.B) {
-      sums_of(a)[b] = {carry.x + from.x, carry.y + from.y};
-      held_of(a)[b] = c.held;
-    }
-    carry.x += total.x, carry.y += total.y;
+// The sums of requests blockIdx.x * tile .. + tile - 1 (at most 1024 of them),
+// and the pages that these give back.
+__global__ __launch_bounds__(kPagesThreads) void pages_give_kernel(PagesArgs a, int tile) {
+  __shared__ SumsLds lds;
+  __shared__ int64_t give_from[kPagesThreads];
+  __shared__ int need[kPagesThreads];
+  const int b0 = blockIdx.x * tile, n = min(tile, a.B - b0);
+  // what requests before ours give and take, and what all give
+  int64_t more[3] = {0, 0, 0};
+  for (int b = threadIdx.x; b < a.B; b += kPagesThreads) {
+    const Change c = change_of(a, b, a.held[b]);
+    more[2] += c.give();
+    if (b < b0) more[0] += c.give(), more[1] += c.take();
   }
-  if (threadIdx.x == 0) {
-    const int64_t count = pages_on_stack(a);
-    *static_cast<longlong2*>(a.scratch) = {count + carry.x, min(count + carry.x, int64_t(a.num_pages))};
+  const int b = b0 + threadIdx.x;
+  Change c = {0, 0, true};
+  if (int(threadIdx.x) < n) c = change_of(a, b, a.held[b]);
+  const Sums s = sum_up<3>({c.give(), c.take()}, more, lds);
+  if (int(threadIdx.x) < n) {
+    sums_of(a)[b] = {s.more[0] + s.before.x, s.more[1] + s.before.y};
+    held_of(a)[b] = c.held;
+    give_from[threadIdx.x] = s.before.x;
+    need[threadIdx.x] = c.need;
   }
-}
-
-// Request blockIdx.x's pages that it gives back.
-__global__ __launch_bounds__(kMoveThreads) void pages_give_kernel(PagesArgs a) {
-  const int b = blockIdx.x;
-  const Change c = change_of(a, b, held_of(a)[b]);
-  const int64_t top = static_cast<longlong2*>(a.scratch)->x - 1 - sums_of(a)[b].x;
-  for (int i = blockIdx.y * kMoveThreads + threadIdx.x; i < c.give(); i += gridDim.y * kMoveThreads) {
-    int32_t* const entry = a.table + b * a.table_stride + c.need + i;
-    put_on_stack(a, top - i, *entry);
-    *entry = -1;
-  }
+  __syncthreads();
+  const int64_t count = pages_on_stack(a) + s.more[2];
+  if (b == 0) *static_cast<longlong2*>(a.scratch) = {0, min(count, int64_t(a.num_pages))};
+  give_back(a, b0, n, give_from, need, s.total.x, count - 1 - s.more[0]);
 }
 
 // Request blockIdx.x's pages that it takes, and its rows.
@@ -225,8 +259,9 @@ hipError_t launch_pages(const PagesArgs& a, hipStream_t stream) {
   const int rows = (a.T + a.B - 1) / a.B, most = (rows + kMoveThreads - 1) / kMoveThreads;
   per = per < most ? per : most;
   const dim3 grid(a.B, per < 1 ? 1 : per);
-  hipLaunchKernelGGL(pages_scan_kernel, dim3(1), dim3(kPagesThreads), 0, stream, a);
-  hipLaunchKernelGGL(pages_give_kernel, dim3(a.B, 1), dim3(kMoveThreads), 0, stream, a);
+  // (64 requests a workgroup keep those that give back much apart)
+  const int even = (a.B + 255) / 256, tile = even < 64 ? 64 : even;
+  hipLaunchKernelGGL(pages_give_kernel, dim3((a.B + tile - 1) / tile), dim3(kPagesThreads), 0, stream, a, tile);
   hipLaunchKernelGGL(pages_take_kernel, grid, dim3(kMoveThreads), 0, stream, a);
   return hipGetLastError();
 }
