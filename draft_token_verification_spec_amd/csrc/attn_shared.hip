@@ -61,11 +61,14 @@ __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, S
   const int b = request_of(a, tok, uniform_at, token0, next);
   if (b < 0) return;
   const PartsOf<M, ALIGN> rows(a, p, b, token0, next);
+  // (the same for all rows of a tile, of which a request mostly has one)
+  const bool one_tile = int64_t(next - token0) * (a.q_heads / a.cache.heads) <= M;
+  int parts, first;
+  rows.of(tok, head0, parts, first);
   const int ch = min(CH * lane, D - CH);
   for (int head = head0; head < min(head0 + heads_at, a.q_heads); ++head) {
     const int64_t at = int64_t(tok) * a.q_heads + head;
-    int parts, first;
-    rows.of(tok, head, parts, first);
+    if (!one_tile) rows.of(tok, head, parts, first);
     const auto index = [&](int i) { return int64_t(i < rows.shared ? i : first + i) * all + at; };
     float top = -INFINITY, total = 0.f;
     Some y = 0.f;
@@ -139,8 +142,10 @@ void launch_join_shared(const AttnArgs& a, const SharedPlan& p, hipStream_t stre
     hipLaunchKernelGGL((join_few_shared_kernel<M, ALIGN>), dim3(a.T, a.q_heads), dim3(kAttnThreads), 0, stream, a, p);
     return;
   }
-  // several heads a wave where the waves fill the card all the same
-  const int heads_at = rows <= 32768 ? 1 : rows <= 131072 ? 4 : 8;
+  // several heads a wave, which then looks its request up once for them, where
+  // the waves fill the card all the same (40960 rows of 2 parts: one 40 us, four
+  // 22.6, eight 21.5)
+  const int heads_at = rows <= 32768 ? 1 : 8;
   const int64_t waves = int64_t(a.T) * ((a.q_heads + heads_at - 1) / heads_at);
   const dim3 grid(int((waves + kAttnWaves - 1) / kAttnWaves)), block(kAttnThreads);
   if (a.cache.D <= 128)
