@@ -16,6 +16,9 @@
 // Otherwise two launches: the sums with the pages given back, by up to 256
 // workgroups, each of which adds up all requests for itself, and the pages taken
 // with the slots, by workgroups of one request each.
+//
+// Measured: 256 requests that grow by 5 tokens 6.5 us; 1500 prompts of up to 1000
+// tokens (55 thousand pages, 940 thousand rows) 7 + 7 us, and given back 10 + 4.
 #include "sv_attn.hpp"
 
 namespace sv {
@@ -98,12 +101,14 @@ __device__ __forceinline__ int last_upto(const E* v, int n, X x) {
   return lo;
 }
 
-// The workgroup's pages given back: the k-th of `total`, of the last request r of
-// n with from[r] <= k, to place top - k of the stack.  Four a thread at a time.
+// The pages given back by n requests from b0 on: the k-th of `total`, of the last
+// request r with from[r] <= k, to place top - k of the stack; by `slices`
+// workgroups, four a thread at a time.
 __device__ __forceinline__ void give_back(const PagesArgs& a, int b0, int n, const int64_t* from, const int* need,
-                                          int64_t total, int64_t top) {
+                                          int64_t total, int64_t top, int slice, int slices) {
   constexpr int kAtATime = 4;
-  for (int64_t k0 = threadIdx.x; k0 < total; k0 += kAtATime * kPagesThreads) {
+  for (int64_t k0 = int64_t(slice) * kAtATime * kPagesThreads + threadIdx.x; k0 < total;
+       k0 += int64_t(slices) * kAtATime * kPagesThreads) {
     int32_t* entry[kAtATime];
     int page[kAtATime];
 #pragma unroll
@@ -166,7 +171,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_small_kernel(PagesArgs a)
   __syncthreads();  // (all have read the count)
   const bool crosses = live && upto > count && from.y <= count;  // the first request that is refused
   if (crosses || (b == a.B - 1 && upto <= count)) *a.free_count = int(count - (crosses ? from.y : upto));
-  give_back(a, 0, a.B, give_from, now, total.x, count0 + total.x - 1);
+  give_back(a, 0, a.B, give_from, now, total.x, count0 + total.x - 1, 0, 1);
   __syncthreads();
   for (int64_t k = b; k < min(total.y, count); k += kPagesThreads) {
     const int r = last_upto(take_from, a.B, k);
@@ -188,7 +193,7 @@ __device__ __forceinline__ longlong2* sums_of(const PagesArgs& a) { return stati
 __device__ __forceinline__ int32_t* held_of(const PagesArgs& a) { return reinterpret_cast<int32_t*>(sums_of(a) + a.B); }
 
 // The sums of requests blockIdx.x * tile .. + tile - 1 (at most 1024 of them),
-// and the pages that these give back.
+// and the pages that these give back, by gridDim.y workgroups.
 __global__ __launch_bounds__(kPagesThreads) void pages_give_kernel(PagesArgs a, int tile) {
   __shared__ SumsLds lds;
   __shared__ int64_t give_from[kPagesThreads];
@@ -206,15 +211,17 @@ __global__ __launch_bounds__(kPagesThreads) void pages_give_kernel(PagesArgs a, 
   if (int(threadIdx.x) < n) c = change_of(a, b, a.held[b]);
   const Sums s = sum_up<3>({c.give(), c.take()}, more, lds);
   if (int(threadIdx.x) < n) {
-    sums_of(a)[b] = {s.more[0] + s.before.x, s.more[1] + s.before.y};
-    held_of(a)[b] = c.held;
+    if (blockIdx.y == 0) {
+      sums_of(a)[b] = {s.more[0] + s.before.x, s.more[1] + s.before.y};
+      held_of(a)[b] = c.held;
+    }
     give_from[threadIdx.x] = s.before.x;
     need[threadIdx.x] = c.need;
   }
   __syncthreads();
   const int64_t count = pages_on_stack(a) + s.more[2];
-  if (b == 0) *static_cast<longlong2*>(a.scratch) = {0, min(count, int64_t(a.num_pages))};
-  give_back(a, b0, n, give_from, need, s.total.x, count - 1 - s.more[0]);
+  if (b == 0 && blockIdx.y == 0) *static_cast<longlong2*>(a.scratch) = {0, min(count, int64_t(a.num_pages))};
+  give_back(a, b0, n, give_from, need, s.total.x, count - 1 - s.more[0], blockIdx.y, gridDim.y);
 }
 
 // Request blockIdx.x's pages that it takes, and its rows.
@@ -261,7 +268,8 @@ hipError_t launch_pages(const PagesArgs& a, hipStream_t stream) {
   const dim3 grid(a.B, per < 1 ? 1 : per);
   // (64 requests a workgroup keep those that give back much apart)
   const int even = (a.B + 255) / 256, tile = even < 64 ? 64 : even;
-  hipLaunchKernelGGL(pages_give_kernel, dim3((a.B + tile - 1) / tile), dim3(kPagesThreads), 0, stream, a, tile);
+  const int tiles = (a.B + tile - 1) / tile, slices = tiles >= 128 ? 1 : tiles > 8 ? 128 / tiles : 16;
+  hipLaunchKernelGGL(pages_give_kernel, dim3(tiles, slices), dim3(kPagesThreads), 0, stream, a, tile);
   hipLaunchKernelGGL(pages_take_kernel, grid, dim3(kMoveThreads), 0, stream, a);
   return hipGetLastError();
 }
