@@ -80,6 +80,18 @@ __device__ __forceinline__ int paired(const Lane& l, int e) {
 }
 __device__ __forceinline__ int angle_of(const Lane& l, int e) { return l.interleaved ? e >> 1 : e < l.half ? e : e - l.half; }
 
+// Where LDS has the e-th angle and the weight of channel e.  VEC: what a lane
+// reads in 16 bytes lies next to what its neighbours read along with it.
+template <bool VEC>
+__device__ __forceinline__ int angle_slot(const Lane& l, int e) {
+  if (!VEC) return e;
+  return l.interleaved ? ((e >> 1 & 1) * (l.half >> 2) + (e >> 2)) * 2 + (e & 1)
+                       : ((e >> 1 & 3) * (l.half >> 3) + (e >> 3)) * 2 + (e & 1);
+}
+__device__ __forceinline__ int weight_slot(int e) {
+  return (e >> 2 & 1) * (SV_ATTN_MAX_HEAD_DIM / 2) + (e >> 3) * 4 + (e & 3);
+}
+
 // A lane's 8 channels of a row as they are asked for, and as floats.  VEC: rows
 // are 16-byte aligned, and heads and turned channels come in whole groups of 8;
 // a lane beyond the row asks for its last channels.  (Interleaved pairs lie in
@@ -141,20 +153,20 @@ __device__ __forceinline__ void turn8(F (&y)[8], const F (&z)[8], const Lane& l,
     }
   } else if (l.e0 < l.rotary) {
     if (l.interleaved) {
-      const F2* at = cs + (l.e0 >> 1);
+      const F2* at = cs + (l.e0 >> 3) * 2;
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const F2 t = at[j >> 1];
+        const F2 t = at[(j >> 2) * (l.half >> 2) * 2 + (j >> 1 & 1)];
         const F a = y[j], c = y[j + 1];
         y[j] = fma(a, t.x, -(c * t.y));
         y[j + 1] = fma(c, t.x, a * t.y);
       }
     } else {
       const bool first = l.e0 < l.half;
-      const F2* at = cs + (first ? l.e0 : l.e0 - l.half);
+      const F2* at = cs + ((first ? l.e0 : l.e0 - l.half) >> 3) * 2;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const F2 t = at[j];
+        const F2 t = at[(j >> 1) * (l.half >> 3) * 2 + (j & 1)];
         y[j] = fma(y[j], t.x, first ? -(z[j] * t.y) : z[j] * t.y);
       }
     }
@@ -172,7 +184,7 @@ __device__ __forceinline__ void stage_weights(Weights& w, const NormWeights& n, 
       float x = e < D ? 1.f : 0.f;
       if (p && e < D)
         x = n.dtype == SV_BF16 ? load1(static_cast<const uint16_t*>(p) + e) : load1(static_cast<const float*>(p) + e);
-      w[k][e] = x;
+      w[k][weight_slot(e)] = x;
     }
 }
 
@@ -181,10 +193,10 @@ __device__ __forceinline__ void times_weights(F (&y)[8], const Lane& l, const fl
   if (VEC) {
   const int e = pairs ? paired(l, l.e0) : l.e0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= w[e + j];
+    for (int j = 0; j < 8; ++j) y[j] *= w[weight_slot(e) + (j >> 2) * (SV_ATTN_MAX_HEAD_DIM / 2) + (j & 3)];
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= w[pairs && l.e0 + j < l.D ? paired(l, l.e0 + j) : l.e0 + j];
+    for (int j = 0; j < 8; ++j) y[j] *= w[weight_slot(pairs && l.e0 + j < l.D ? paired(l, l.e0 + j) : l.e0 + j)];
   }
 }
 
@@ -226,12 +238,13 @@ struct Item {
 };
 
 // mscale * (cos, sin) of the angles of rows t0 .. t0 + rows - 1.
-template <int ROWS>
-__device__ __forceinline__ void angles_of_rows(float2 (*cs)[kMaxPairs], const NormRopeArgs& a, int t0, int rows, float sign) {
-  const int pairs = a.rotary >> 1;
+template <int ROWS, bool VEC>
+__device__ __forceinline__ void angles_of_rows(float2 (*cs)[kMaxPairs], const NormRopeArgs& a, const Lane& l, int t0,
+                                               int rows, float sign) {
+  const int pairs = l.half;
   for (int i = threadIdx.x; i < ROWS * pairs; i += kRopeThreads) {
     const int r = ROWS == 1 ? 0 : i / pairs, e = i - r * pairs;
-    if (r < rows) cs[r][e] = turn_of(double(a.positions[t0 + r]), a.freq[e], a.mscale, sign);
+    if (r < rows) cs[r][angle_slot<VEC>(l, e)] = turn_of(double(a.positions[t0 + r]), a.freq[e], a.mscale, sign);
   }
 }
 
@@ -251,8 +264,8 @@ __device__ __forceinline__ auto row_of(const NormRopeArgs& a, const Rows& q, con
 
 template <int LG, int ROWS, bool VEC, typename ET>
 __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(NormRopeArgs a) {
-  __shared__ float2 cs[ROWS][kMaxPairs];
-  __shared__ Weights w;
+  __shared__ __align__(16) float2 cs[ROWS][kMaxPairs];
+  __shared__ __align__(16) Weights w;
   const int t0 = blockIdx.x * ROWS, rows = min(ROWS, a.T - t0);
   const Lane l = lane_of<LG>(a.D, a.rotary, a.layout);
   const int total = a.q_heads + a.k_heads;
@@ -265,7 +278,7 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(NormRopeArgs a)
     z0.ask(x, l, true);
   }
   stage_weights(w, a.norm, a.D);
-  angles_of_rows<ROWS>(cs, a, t0, rows, 1.f);
+  angles_of_rows<ROWS, VEC>(cs, a, l, t0, rows, 1.f);
   __syncthreads();
   while (it.row < rows) {
     float y[8], z[8];
@@ -288,8 +301,8 @@ constexpr int kMostParts = 1024;  // workgroups of the backward pass: 16 waves a
 
 template <int LG, int ROWS, bool VEC, typename ET>
 __global__ __launch_bounds__(kRopeThreads) void norm_rope_backward_kernel(NormRopeArgs a) {
-  __shared__ float2 cs[2][ROWS][kMaxPairs];
-  __shared__ Weights w;
+  __shared__ __align__(16) float2 cs[2][ROWS][kMaxPairs];
+  __shared__ __align__(16) Weights w;
   __shared__ float sums[kRopeThreads / 64][2][8 << LG];
   const Lane l = lane_of<LG>(a.D, a.rotary, a.layout);
   const int total = a.q_heads + a.k_heads;
@@ -310,7 +323,7 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_backward_kernel(NormRo
       z0.ask(dy, l, true);
     };
     if (it.row < rows) ask(it);
-    angles_of_rows<ROWS>(cs[buf], a, t0, rows, -1.f);
+    angles_of_rows<ROWS, VEC>(cs[buf], a, l, t0, rows, -1.f);
     __syncthreads();
     while (it.row < rows) {
       float x[8], g[8], z[8];
@@ -427,9 +440,9 @@ __device__ __forceinline__ void norm_and_turn_key8(float (&y)[8], const float (&
 // waves (85 to 98 us, 13 to 16).
 template <int LG, bool VEC, bool FP8, typename ET>
 __global__ __launch_bounds__(kRopeThreads, VEC ? 5 : 4) void append_normed_kernel(AppendArgs a) {
-  __shared__ float2 cs[kMaxPairs];
+  __shared__ __align__(16) float2 cs[kMaxPairs];
   __shared__ double2 exact[kMaxPairs];
-  __shared__ Weights w;
+  __shared__ __align__(16) Weights w;
   const PagedView& cache = a.cache;
   const int t = blockIdx.x, heads = cache.heads;
   // requests of equally many rows are found at once, others by a search
@@ -449,8 +462,9 @@ __global__ __launch_bounds__(kRopeThreads, VEC ? 5 : 4) void append_normed_kerne
   for (int i = threadIdx.x; i < l.half; i += kRopeThreads) {
     double s, c;
     sincospi(half_turns(position, a.freq[i]), &s, &c);
-    exact[i] = make_double2(c * a.mscale, s * a.mscale);
-    cs[i] = make_float2(float(c * a.mscale), float(s * a.mscale));
+    const int at = angle_slot<VEC>(l, i);
+    exact[at] = make_double2(c * a.mscale, s * a.mscale);
+    cs[at] = make_float2(float(c * a.mscale), float(s * a.mscale));
   }
   __syncthreads();
 

@@ -333,7 +333,9 @@ int sv_paged_attention_sinks(void* stream, int B, int T, int q_heads, const void
                              size_t workspace_bytes);
 
 /* Bytes of workspace that sv_paged_attention_shared needs (256: none); 0 for
- * sizes that the call would reject. */
+ * sizes that the call would reject.  Every row has a part for each split of the
+ * shared and of the own tokens, at least one of either: 4 (head_dim + 2) bytes a
+ * part, token and query head. */
 size_t sv_paged_attention_shared_workspace_size(int B, int T, int groups, int q_heads, int kv_heads, int head_dim,
                                                 int max_q_len, int max_group_len, int max_shared_len, int max_own_len);
 

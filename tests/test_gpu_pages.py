@@ -185,3 +185,26 @@ def test_many_requests_scratch():
         assert (ws[size:] == 255).all()
     with pytest.raises(RuntimeError, match="workspace"):
         pool.step([0] * B, workspace=ws[:size - 1])
+
+
+def test_largest_batch():
+    """2^18 requests: up, partly refused, and down."""
+    B = 1 << 18
+    pool = Pool(B, 3, B, 4, seed=1)
+    rng = np.random.default_rng(2)
+    first = rng.integers(0, 7, B)
+    granted = pool.step(first.tolist())
+    assert 0 < sum(granted) < B
+    start = np.minimum(np.arange(B + 1) * 2, 100000).tolist()
+    pool.step((first // 2).tolist(), start, 100000)
+    pool.step([0] * B)
+    assert len(pool.free) == B
+
+
+def test_one_long_context_given_back():
+    """Pages of one request by several workgroups, among requests that hold few; and with few rows by one."""
+    for rows in (9000, 3):
+        pool = Pool(40, 20000, 21000, 16, seed=4)
+        pool.step([16 * (i % 5) for i in range(39)] + [16 * 20000 - 3])
+        start = np.minimum(np.arange(41) * 230, rows).tolist()
+        pool.step([16 * (i % 3) for i in range(39)] + [100], start, rows)
