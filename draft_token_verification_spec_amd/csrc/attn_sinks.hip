@@ -1,6 +1,14 @@
 // Attention over a paged cache with a sliding window and a few first tokens that
 // stay visible: the kernels of sv_attn_kernels.hpp over a range of tokens with a
-// gap between the two.
+// gap between the two.  Both ends of the gap lie on whole pieces of 32 (few rows)
+// or 64 tokens, so that no load spans it; what a piece holds beyond the first
+// tokens or before the window is masked.
+//
+// Bound as the kernels are: 64 requests of 7500 to 30000 bf16 tokens, window
+// 2048 and 4 first tokens, 8 heads of 128 channels under 32 queries each, 539 MB
+// in 106 us and 10 of joining (4.65 TB/s); 2048 new tokens behind 8192 8-bit ones,
+// window 4096 and 128 first tokens, 142 GFLOP in 158 to 168 us (840 to 900
+// TFLOP/s); one token behind 100000, window 4096, 9 + 4 us (latency).
 #include "sv_attn_kernels.hpp"
 
 namespace sv {

@@ -19,6 +19,11 @@
 // The weights' gradients are summed by a thread over its heads and rows, by the
 // workgroup in LDS, and by a second kernel over the workgroups, each in a fixed
 // order.
+//
+// Measured: 64 rows of 32 + 8 heads of 128 bf16 channels 5.4 us (latency: a
+// launch, the position, the angles); gradients of 8191 such rows, 252 MB in 52 +
+// 5 us (4.8 TB/s; a plain copy reaches 5.1; their 28.7 million wave instructions
+// alone take 47 us).
 #include "sv_rope.hpp"
 
 namespace sv {
@@ -517,7 +522,10 @@ bool vec_of(const NormRopeArgs& a, int elem, bool backward) {
 }
 
 // Rows that a workgroup takes at a time: several where there are enough to fill
-// the card with.
+// the card with, whose angles then keep all threads busy and whose heads divide
+// into whole turns of its groups (bf16, 40 heads of 128, whole calls: 8191 rows'
+// gradients 66 us one row at a time and 57 four, 16000 rows 81 and 69; of 64
+// channels 46 and 35; below 4000 rows no difference).
 constexpr int kManyRowsAtATime = 4;
 bool many(int T) { return T >= 1024 * kManyRowsAtATime; }
 
