@@ -153,8 +153,8 @@ void launch_join_shared(const AttnArgs& a, const SharedPlan& p, hipStream_t stre
   }
   // several heads a wave, which then looks its request up once for them, where
   // the waves fill the card all the same (40960 rows of 2 parts: one 40 us, four
-  // 22.6, eight 21.5)
-  const int heads_at = rows <= 32768 ? 1 : 8;
+  // 22.6, eight 21.5; 17460 rows of 2 to 4 one 18, four 12; 4096 rows of 9 one 8)
+  const int heads_at = rows <= 8192 ? 1 : rows <= 32768 ? 4 : 8;
   const int64_t waves = int64_t(a.T) * ((a.q_heads + heads_at - 1) / heads_at);
   const dim3 grid(int((waves + kAttnWaves - 1) / kAttnWaves)), block(kAttnThreads);
   if (a.cache.D <= 128)
