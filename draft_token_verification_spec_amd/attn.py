@@ -330,15 +330,16 @@ def sv_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, lay
     return out
 
 
-def _two(dev: int, name: str, q, k, T: int, D: int, dtype):
+def _two(dev: int, names, q, k, T: int, D: int, dtype):
     """Rows of queries and keys (no keys: k is None): (q, its heads, k, its heads)."""
     q_heads = q.shape[1]
-    qr = _rows(dev, name.format("q"), q, dtype, (T, q_heads, D))
+    qr = _rows(dev, names[0], q, dtype, (T, q_heads, D))
     if k is None:
         return qr, q_heads, (None, 0, 0), 0
-    _tensor(name.format("k"), k)
-    k_heads = _three(name.format("k"), k)[1]
-    return qr, q_heads, _rows(dev, name.format("k"), k, dtype, (T, k_heads, D)), k_heads
+    if not isinstance(k, torch.Tensor):
+        _tensor(names[1], k)
+    k_heads = _three(names[1], k)[1]
+    return qr, q_heads, _rows(dev, names[1], k, dtype, (T, k_heads, D)), k_heads
 
 
 def _outputs(dev: int, o: dict, names, like, T: int, D: int, dtype):
@@ -347,13 +348,12 @@ def _outputs(dev: int, o: dict, names, like, T: int, D: int, dtype):
     for name, x in zip(names, like):
         if x is None:
             rows.append((None, 0, 0))
-            continue
-        shape = (T, x.shape[1], D)
-        if name in o:
-            rows.append(_rows(dev, f"out['{name}']", o[name], dtype, shape))
+        elif name in o:
+            rows.append(_rows(dev, f"out['{name}']", o[name], dtype, (T, x.shape[1], D)))
         else:
-            t = o[name] = _new(shape, dtype, x.device)
-            rows.append((t.data_ptr(), shape[1] * D, D))
+            heads = x.shape[1]
+            t = o[name] = torch.empty_strided((T, heads, D), (heads * D, D, 1), dtype=dtype, device=x.device)
+            rows.append((t.data_ptr(), heads * D, D))
     return rows
 
 
@@ -381,7 +381,7 @@ def sv_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optio
     T, _, D = _three("q", q)
     dtype = q.dtype
     code = _dtype_code("q", dtype)
-    qr, q_heads, kr, k_heads = _two(dev, "{}", q, k, T, D, dtype)
+    qr, q_heads, kr, k_heads = _two(dev, ("q", "k"), q, k, T, D, dtype)
     pos, fp, rotary = _turns(dev, T, positions, freq)
     weights = _weights(dev, D, q_weight, k_weight)
     o = {} if out is None else out
@@ -410,12 +410,12 @@ def sv_qk_norm_rope_backward(q: torch.Tensor, k: Optional[torch.Tensor], dq_out:
     T, _, D = _three("q", q)
     dtype = q.dtype
     code = _dtype_code("q", dtype)
-    qr, q_heads, kr, k_heads = _two(dev, "{}", q, k, T, D, dtype)
+    qr, q_heads, kr, k_heads = _two(dev, ("q", "k"), q, k, T, D, dtype)
     _tensor("dq_out", dq_out)
     _three("dq_out", dq_out)
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
-    gqr, gq_heads, gkr, gk_heads = _two(dev, "d{}_out", dq_out, dk_out, T, D, dtype)
+    gqr, gq_heads, gkr, gk_heads = _two(dev, ("dq_out", "dk_out"), dq_out, dk_out, T, D, dtype)
     if gq_heads != q_heads or gk_heads != k_heads:
         raise ValueError(f"dq_out and dk_out have {gq_heads} and {gk_heads} heads, q and k {q_heads} and {k_heads}")
     pos, fp, rotary = _turns(dev, T, positions, freq)
