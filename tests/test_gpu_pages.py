@@ -208,3 +208,24 @@ def test_one_long_context_given_back():
         pool.step([16 * (i % 5) for i in range(39)] + [16 * 20000 - 3])
         start = np.minimum(np.arange(41) * 230, rows).tolist()
         pool.step([16 * (i % 3) for i in range(39)] + [100], start, rows)
+
+
+def test_outputs_that_are_not_asked_for():
+    """The C call with any of granted, slots and positions missing moves the same pages and writes the others alike."""
+    from draft_token_verification_spec_amd import attn
+
+    lens, start, T = [33, 7, 0, 50], [0, 3, 4, 4, 9], 9
+    want = Pool(4, 6, 20, 16, seed=2)
+    want.step(lens, start, T)
+    o = sv.sv_kv_pages(want.d_table, want.d_held, want.d_free, want.d_count, I32(lens), page_size=16, query_start=I32(start),
+                       rows=T)
+    for asked in range(8):
+        pool = Pool(4, 6, 20, 16, seed=2)
+        out = [torch.full((n,), -77, dtype=t, device="cuda") for n, t in ((4, torch.int32), (T, torch.int64), (T, torch.int64))]
+        ptr = [x.data_ptr() if asked >> i & 1 else None for i, x in enumerate(out)]
+        kl, qs = I32(lens), I32(start)
+        attn._call(0, "sv_kv_pages", 4, T, 16, 6, 20, kl.data_ptr(), None, qs.data_ptr(), pool.d_table.data_ptr(),
+                   pool.d_table.stride(0), pool.d_held.data_ptr(), pool.d_free.data_ptr(), pool.d_count.data_ptr(), *ptr, None, 0)
+        assert torch.equal(pool.d_table, want.d_table) and torch.equal(pool.d_held, want.d_held)
+        for i, n in enumerate(("granted", "slots", "positions")):
+            assert torch.equal(out[i], o[n]) if asked >> i & 1 else (out[i] == -77).all(), (asked, n)
