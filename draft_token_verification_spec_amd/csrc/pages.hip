@@ -13,9 +13,10 @@
 // Bound by latency: a scan and three dependent copies.  Up to 1024 requests
 // and kSmallRows rows one workgroup does it all, the copies shared evenly over
 // its threads, each of which finds its item's request by a search in LDS.
-// Otherwise two launches: the sums with the pages given back, by up to 256
-// workgroups, each of which adds up all requests for itself, and the pages taken
-// with the slots, by workgroups of one request each.
+// Otherwise two launches: the sums with the pages given back, by workgroups of
+// 64 requests or more (several for one such part, where there are few), each of
+// which adds up all requests for itself, and the pages taken with the slots, by
+// workgroups of one request each.
 //
 // Measured: 256 requests that grow by 5 tokens 6.5 us; 1500 prompts of up to 1000
 // tokens (55 thousand pages, 940 thousand rows) 7 + 7 us, and given back 10 + 4.
@@ -245,8 +246,10 @@ __global__ __launch_bounds__(kMoveThreads) void pages_take_kernel(PagesArgs a) {
     put_row(a, int(t), b, len - (end - t), now, c.held, from, count);
 }
 
-// Rows that one workgroup takes along.
-constexpr int kSmallRows = 8192;
+// Rows that one workgroup takes along (a step taken and given back, one launch
+// and two: 256 requests of 1280 rows 15.6 and 20.1 us, a prompt of 4000 14.4 and
+// 17.8; 1000 requests of 5000 rows 24.5 and 22.0, 256 of 10394 34.7 and 20.3).
+constexpr int kSmallRows = 4096;
 
 bool small(int B, int T) { return B <= kPagesThreads && T <= kSmallRows; }
 
