@@ -133,17 +133,24 @@ __device__ __forceinline__ int shared_tokens(const AttnArgs& a, int g, Load load
   return int(min(int64_t(max(load(a.shared_len, g), 0)), int64_t(a.cache.max_pages) << a.cache.page_shift));
 }
 
+// Whether a group of the requests first .. next - 1 is within the batch: no other
+// shares anything, neither where its tokens are read nor where its parts are joined.
+__device__ __forceinline__ bool group_stands(const AttnArgs& a, int first, int next) {
+  return first >= 0 && first < next && next <= a.B;
+}
+
 // The tokens that request b shares: those of the group that it is in, if any.
 // Groups of equally many requests are found at once, others by a search of the
 // whole wave.
 __device__ __forceinline__ int shared_tokens_of(const AttnArgs& a, int b) {
   int g = int(int64_t(b) * a.groups / a.B);
-  const int first = uniform_at(a.group_start, g), next = uniform_at(a.group_start, g + 1);
+  int first = uniform_at(a.group_start, g), next = uniform_at(a.group_start, g + 1);
   const int shared = shared_tokens(a, g, uniform_at);
-  if (b >= first && b < next) return shared;
+  if (b >= first && b < next) return group_stands(a, first, next) ? shared : 0;
   g = uniform(find_sequence(a.group_start, a.groups, b, threadIdx.x & 63));
-  if (g < 0 || b >= uniform_at(a.group_start, g + 1)) return 0;
-  return shared_tokens(a, g, uniform_at);
+  if (g < 0) return 0;
+  first = uniform_at(a.group_start, g), next = uniform_at(a.group_start, g + 1);
+  return b < next && group_stands(a, first, next) ? shared_tokens(a, g, uniform_at) : 0;
 }
 
 // The tile of a request of n rows from token0 on and len cached tokens, the
@@ -188,7 +195,7 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs& a, int G, int b, int64_t
   if constexpr (PART == Part::kShared) {
     const int first = uniform_at(a.group_start, b), next = uniform_at(a.group_start, b + 1);
     t.rows = 0;
-    if (first < 0 || next > a.B || first >= next) return t;
+    if (!group_stands(a, first, next)) return t;
     const int token0 = uniform_at(a.query_start, first);
     const int64_t n = int64_t(uniform_at(a.query_start, next)) - token0, rows = n * G - first_row;
     if (token0 < 0 || int64_t(token0) + n > a.T || rows <= 0) return t;

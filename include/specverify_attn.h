@@ -348,7 +348,8 @@ size_t sv_paged_attention_shared_workspace_size(int B, int T, int groups, int q_
  * j if j <= its place, as any other.
  *   groups     0: nothing is shared.
  *   group_start    int32 [groups + 1], ascending, within 0..B; requests outside
- *              group_start[0] .. group_start[groups] - 1 share nothing.
+ *              group_start[0] .. group_start[groups] - 1 share nothing, nor do
+ *              those of a group that reaches beyond the batch.
  *   shared_len     int32 [groups]; negative counts as 0.  The first request's row
  *              has to hold the shared pages also where that request has no rows,
  *              or a kv_len below shared_len.
