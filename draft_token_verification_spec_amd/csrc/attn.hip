@@ -52,9 +52,9 @@ AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_
   int64_t ranges = (max_kv_len + 16383) / 16384 < 8 ? (max_kv_len + 16383) / 16384 : 8;
   if (part_bytes * ranges > kMostParts) ranges = kMostParts / part_bytes;
   if (p.row_tile <= 32 && n < ranges) n = ranges;
-  // Contexts of one length need no more than the compute units' places, two each,
-  // nearly filled once (64 requests of 8 heads that see 2052 tokens: 117 us in 4
-  // splits, 109 in one; of 5 8-bit new tokens 92 in two, 66 in one; 24 of 4100
+  // Short contexts of one length need no more than the compute units' places, two
+  // each, nearly filled once (64 requests of 8 heads that see 2052 tokens: 117 us
+  // in 4 splits, 109 in one; of 5 8-bit new tokens 92 in two, 66 in one; 24 of 4100
   // tokens, which fill three eighths: 86 in 11, 92 in 3).
   if (even && groups >= 448) n = 1;
   if (n < 1 || max_kv_len <= 512) n = 1;

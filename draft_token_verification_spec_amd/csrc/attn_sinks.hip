@@ -13,6 +13,19 @@
 
 namespace sv {
 
+// Tokens up to which a tile's reach makes contexts even, for each of its rows: a
+// batch of 64 requests, 8 heads each, whose contexts are all longer than the
+// window / of all lengths up to that / one as long and 63 of 300 tokens, in us,
+// undivided and divided,
+//   16 rows a tile (one new token, bf16)   32 rows (5 new tokens, 8-bit)
+//   1024   54 39 28    58 46 34               35  27 22    64  49 34
+//   2048  110 74 42   116 71 39               59  42 32    84  63 39
+//   4096  207 154 69  206 133 52             119  87 50   141  99 49
+//   8192  400 299 123 381 245 76             225 174 86   244 173 75
+//  16384  787 593 234 735 470 120            438 336 160  439 310 118
+// (and 65536 tokens, one row: 3116 2342 954, divided 2837 1762 350).
+constexpr int kEvenTokensARow = 256;
+
 // A tile of rows reads the first tokens, its window's and its own rows' at most:
 // contexts are divided as if they were all as long as that (with the pieces of
 // tokens that the ends of the two lie in), and no longer.
@@ -20,7 +33,9 @@ AttnPlan plan_sinks(int B, int T, int q_heads, int kv_heads, int D, int max_q_le
   const AttnPlan p = plan_attention(B, T, q_heads, kv_heads, D, max_q_len, max_kv_len);
   if (window == 0) return p;
   const int64_t reach = int64_t(window) + sinks + p.row_tile / (q_heads / kv_heads) + 2 * kTile;
-  return reach < max_kv_len ? plan_attention(B, T, q_heads, kv_heads, D, max_q_len, int(reach), true) : p;
+  if (reach >= max_kv_len) return p;
+  const bool even = reach <= int64_t(kEvenTokensARow) * (p.row_tile < 32 ? p.row_tile : 32);
+  return plan_attention(B, T, q_heads, kv_heads, D, max_q_len, int(reach), even);
 }
 
 hipError_t launch_sinks(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream) {

@@ -146,7 +146,7 @@ struct AttnPlan {
   float2* part_ml;  // maximum (base-2 logarithm), sum of weights
   float* part_o;    // weighted values
 };
-// even: contexts are (nearly) of one length.
+// even: contexts are short, and (nearly) of one length.
 AttnPlan plan_attention(int B, int T, int q_heads, int kv_heads, int D, int max_q_len, int max_kv_len,
                         bool even = false);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int cache_dtype, hipStream_t stream);
