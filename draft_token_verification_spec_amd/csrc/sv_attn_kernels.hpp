@@ -1237,14 +1237,16 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(AttnArgs a, AttnPlan
 
 // Up to 4096 workgroups, twice what the card holds: where few of many rows were
 // split, a workgroup for each would cost more than the joining (164 thousand
-// rows: 250 us).
+// rows: 250 us).  (Shared and own parts are joined together, attn_shared.hip.)
 template <int M, Part PART, int ALIGN>
 void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  if (p.num_splits == 1 || !is_whole(PART)) return;
-  const int64_t all = int64_t(a.T) * a.q_heads;
-  const int per = int((all + 4095) / 4096);
-  const dim3 grid(int((all + per - 1) / per)), block(kAttnThreads);
-  hipLaunchKernelGGL((join_kernel<M, PART, ALIGN>), grid, block, 0, stream, a, p, per);
+  if constexpr (is_whole(PART)) {
+    if (p.num_splits == 1) return;
+    const int64_t all = int64_t(a.T) * a.q_heads;
+    const int per = int((all + 4095) / 4096);
+    const dim3 grid(int((all + per - 1) / per)), block(kAttnThreads);
+    hipLaunchKernelGGL((join_kernel<M, PART, ALIGN>), grid, block, 0, stream, a, p, per);
+  }
 }
 
 template <int DP, int MT, bool FP8, bool SMALL, Part PART>
