@@ -419,14 +419,18 @@ __device__ __forceinline__ float shortened(double x) {
 
 // y (and z) normed and turned in binary64: keys, which are stored once and read
 // by every later row, are so the nearest 8-bit values (FP8; in binary32 some
-// 10^-6 of them are not), or the nearest binary32 ones on their way to bf16.
+// 10^-6 of them are not), or the nearest binary32 ones on their way to bf16, for
+// finite rows of any size.  The root is the hardware's binary64 estimate (some
+// 2^-24 off) and one step of Newton's method.
 template <int LG, bool VEC, bool FP8>
 __device__ __forceinline__ void norm_and_turn_key8(float (&y)[8], const float (&z)[8], const Lane& l, const double2* cs,
                                                    const float* w, const NormWeights& n) {
   double u[8], v[8], sq = 0.;
 #pragma unroll
   for (int j = 0; j < 8; ++j) u[j] = y[j], sq = fma(u[j], u[j], sq);
-  const double r = inverse_root(group_sum<LG>(sq) * n.inv_dim + n.eps);
+  const double m = group_sum<LG>(sq) * n.inv_dim + n.eps;
+  double r = __builtin_amdgcn_rsq(m);  // (the squares of binary32's larger numbers are beyond its range)
+  r *= 1.5 - 0.5 * m * r * r;
   times_weights<VEC>(u, l, w, false);
   if (!VEC || !l.interleaved) {
 #pragma unroll

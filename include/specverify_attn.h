@@ -199,9 +199,11 @@ int sv_qk_norm_rope_backward(void* stream, int T, int q_heads, int k_heads, int 
                              int64_t dq_head_stride, void* dk, int64_t dk_token_stride, int64_t dk_head_stride,
                              float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes);
 
-/* sv_kv_append with norms: keys and queries are normed as by sv_qk_norm_rope
- * before they are turned, in binary32 with one rounding at the end; values are
- * not normed. */
+/* sv_kv_append with norms: keys and queries are normed before they are turned,
+ * values are not.  Queries are formed in binary32 as by sv_qk_norm_rope and
+ * rounded once.  Keys, which every later row reads, are formed in binary64, from
+ * finite rows of any size, and rounded once to SV_E4M3, to SV_BF16 by way of
+ * binary32.  Both may differ by these roundings from what sv_qk_norm_rope gives. */
 int sv_kv_append_normed(void* stream, int B, int T, int q_heads, int dtype, int rotary_dim, int layout,
                         const double* freq, float mscale, const int64_t* positions, int weight_dtype,
                         const void* q_weight, const void* k_weight, float eps, const void* q, int64_t q_token_stride,
