@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, S
   const int D = a.cache.D;
   const int64_t all = int64_t(a.T) * a.q_heads;
   const int turns = (a.q_heads + heads_at - 1) / heads_at;  // of waves for a token
-  const int64_t at_wave = int64_t(blockIdx.x) * kAttnWaves + uniform(threadIdx.x >> 6);
+  const int64_t at_wave = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kAttnWaves + uniform(threadIdx.x >> 6);
   const int tok = uniform(int(at_wave / turns)), head0 = uniform(int(at_wave % turns)) * heads_at;
   if (tok >= a.T) return;
   int token0, next;
@@ -156,7 +156,9 @@ void launch_join_shared(const AttnArgs& a, const SharedPlan& p, hipStream_t stre
   // 22.6, eight 21.5; 17460 rows of 2 to 4 one 18, four 12; 4096 rows of 9 one 8)
   const int heads_at = rows <= 8192 ? 1 : rows <= 32768 ? 4 : 8;
   const int64_t waves = int64_t(a.T) * ((a.q_heads + heads_at - 1) / heads_at);
-  const dim3 grid(int((waves + kAttnWaves - 1) / kAttnWaves)), block(kAttnThreads);
+  // (threads of one dimension of a grid are counted in 32 bits)
+  const int64_t blocks = (waves + kAttnWaves - 1) / kAttnWaves, wide = blocks < (1 << 22) ? blocks : 1 << 22;
+  const dim3 grid(unsigned(wide), unsigned((blocks + wide - 1) / wide)), block(kAttnThreads);
   if (a.cache.D <= 128)
     hipLaunchKernelGGL((join_shared_kernel<M, ALIGN, 2>), grid, block, 0, stream, a, p, heads_at);
   else
