@@ -20,6 +20,16 @@
 // MB in 24 + 6 us (22 + 8 + 6).  What is missing to the read rate: a compute unit
 // has places for two workgroups of either kind, so that while the shared part
 // runs the own one has half of its loads in flight.
+//
+// Where it does not pay: a row has two parts at least, written and read in
+// binary32, and every request a workgroup of its own a head for its own tokens.
+// Prompts (2048 new behind 4096: 296 us, sv_paged_attention 228), short shared
+// parts (177 requests of 4 new behind 40 + 43: 42 and 16) and 256 channels (78
+// behind 182 + 53: 55 and 38) are quicker without sharing.
+//
+// Registers: the few-rows kernels of 128 8-bit channels take 170 to 187 (16 rows),
+// two waves a SIMD for the whole contexts' three; those of 256 bf16 channels spill
+// up to 67 (few rows) and 41 (many rows, pages of fewer than 16 tokens).
 #include "sv_attn_kernels.hpp"
 #include "sv_attn_shared.hpp"
 
@@ -172,10 +182,15 @@ SharedPlan plan_shared(int B, int T, int groups, int q_heads, int kv_heads, int 
   SharedPlan p;
   p.shared = plan_attention(groups, T, q_heads, kv_heads, D, max_group_len, max_shared_len);
   if (p.shared.row_tile > 32) {
-    // A workgroup a compute unit, as far as 256 tokens for each go: the own
-    // parts' take the other places, and every split is a part to be written and
-    // read (128 requests behind 8000: two a compute unit 74 + 10 us, one 66 + 8,
-    // one for two 76 + 7).
+    // A workgroup a compute unit, as far as 256 tokens for each go: where the own
+    // parts are in the same launch, theirs take the other places, and every split
+    // is a part to be written and read (128 requests behind 8000: two a compute
+    // unit 74 + 10 us, one 66 + 8, one for two 76 + 7).  Whole calls in us, so
+    // and with the two a compute unit of plan_attention: 256 requests of 5 new
+    // behind 8 prompts 252 and 278; one part after the other, 64 of 20 new behind
+    // 8000 189 and 214, 88 of 10 behind 13236 248 and 307, 256 channels, 128 behind
+    // 8000 171 and 191.  Against it: 19 of 22 new behind 11392 77 and 69, 4 of 512
+    // behind 4096 216 and 208, 256 channels, 128 of 5 new 8-bit 449 and 389.
     const int64_t tiles = int64_t(groups) * p.shared.tiles * kv_heads;
     int64_t n = tiles > 0 ? (256 + tiles - 1) / tiles : 1;
     const int64_t most = (int64_t(max_shared_len) + 255) / 256;

@@ -5,8 +5,10 @@
 // tokens or before the window is masked.
 //
 // Bound as the kernels are: 64 requests of 7500 to 30000 bf16 tokens, window
-// 2048 and 4 first tokens, 8 heads of 128 channels under 32 queries each, 539 MB
-// in 107 us (4.95 TB/s); 2048 new tokens behind 8192 8-bit ones,
+// 2048 and 4 first tokens, 8 heads of 128 channels under 32 queries in all, 539 MB
+// in 107 us (4.95 TB/s); 128 such requests of 8-bit tokens, 544 MB, in 110 us a
+// call, although the kernel of 16 rows and 128 8-bit channels takes 169 registers
+// or 170, one or two more than let a third wave run on a SIMD; 2048 new tokens behind 8192 8-bit ones,
 // window 4096 and 128 first tokens, 142 GFLOP in 158 to 168 us (840 to 900
 // TFLOP/s); one token behind 100000, window 4096, 9 + 4 us (latency).
 #include "sv_attn_kernels.hpp"

@@ -444,9 +444,12 @@ __device__ __forceinline__ void norm_and_turn_key8(float (&y)[8], const float (&
 
 // One workgroup per row, as rope.hip's append.  Bound by HBM for many rows: 8285
 // binary32 rows of 32 + 8 + 8 heads of 128 into an 8-bit cache, 357 MB in 75 us
-// (4.8 TB/s); by latency for few: 1280 bf16 rows of the same heads 12.5 us.  Four
+// (4.8 TB/s); by latency for few: 1280 bf16 rows of the same heads 11.5 us.  Four
 // rows a workgroup, or a head's channels asked for ahead, cost registers and so
-// waves (85 to 98 us, 13 to 16).
+// waves (85 to 98 us, 13 to 16).  Vector rows are held to the 96 registers of five
+// waves a SIMD, for which up to five are spilled, of a key's binary64 channels.
+// A row's angles, weights and barriers are the same for few heads: 8192 rows of 8 +
+// 1 + 1 heads take 29 us a call for 42 MB, 32768 of 4 + 1 + 1 82 for 101.
 template <int LG, bool VEC, bool FP8, typename ET>
 __global__ __launch_bounds__(kRopeThreads, VEC ? 5 : 4) void append_normed_kernel(AppendArgs a) {
   __shared__ __align__(16) float2 cs[kMaxPairs];

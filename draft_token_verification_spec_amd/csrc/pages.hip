@@ -20,6 +20,10 @@
 //
 // Measured: 256 requests that grow by 5 tokens 6.5 us; 1500 prompts of up to 1000
 // tokens (55 thousand pages, 940 thousand rows) 7 + 7 us, and given back 10 + 4.
+// The pages themselves do not choose the launch: where up to 1024 requests take or
+// give back very many in a call of few rows, one workgroup moves them all (64
+// requests of 131072 tokens, 524 thousand pages, 350 us either way).
+// pages_give_kernel fills the 128 registers of 1024 threads and spills 17.
 #include "sv_attn.hpp"
 
 namespace sv {

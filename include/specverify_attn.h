@@ -360,7 +360,10 @@ size_t sv_paged_attention_shared_workspace_size(int B, int T, int groups, int q_
  *              largest number of tokens of a request that are not shared, as far
  *              as the caller knows them (0: not known; then contexts are not
  *              divided).  They choose how the work is divided, as in
- *              sv_paged_attention. */
+ *              sv_paged_attention.
+ * Worth it where the shared tokens are most of what a request's few rows read;
+ * prompts of many rows, and requests with less in common than of their own, are
+ * quicker with sv_paged_attention, which needs no part of every row either. */
 int sv_paged_attention_shared(void* stream, int B, int T, int q_heads, const void* q, int64_t q_token_stride,
                               int64_t q_head_stride, const sv_paged_cache* cache, const int32_t* query_start,
                               const int32_t* kv_len, int groups, const int32_t* group_start, const int32_t* shared_len,
